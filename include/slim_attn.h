@@ -313,6 +313,129 @@ slim_status slim_attn_decode(const void *q, const void *k, const void *v, const 
 slim_status slim_attn_decode_f32(const float *q, const float *k, const float *v, const float *w, float *state,
                                  float *y, int B, int H, int d, int M, slim_stream_t stream);
 
+/* ---- The rest of a layer in 8 bits ------------------------------------------
+ *
+ * Row-wise operators for the layer around the attention: the norm with the
+ * residual's addition, dense projections, the activation, and the rows the
+ * backward keeps of each, with 8-bit codes in place of 16- or 32-bit values.
+ *
+ * An 8-bit matrix [rows][cols] is two buffers:
+ *   codes   e4m3 (sign, 4 exponent bits with bias 7, 3 fraction bits),
+ *           [rows][128 * nb], nb = ceil(cols / 128); columns past `cols` are
+ *           zero; 16-byte aligned;
+ *   scales  bytes [ceil(rows / R)][4 * ceil(nb / 4)], one for each R rows and
+ *           128 columns (R = 1, or 128 for a packed weight); bytes past nb are
+ *           127; 4-byte aligned.
+ * The value of a code is code * 2^(scale - 127).  The library writes
+ * scale - 127 = e, the smallest integer in [-117, 120] for which the block's
+ * largest magnitude is at most 448 * 2^e, and rounds to nearest, ties to even
+ * (for e = 120 to at most 240, so that every value is a finite fp32 number).
+ * A power of two makes every value exact in bf16 (and the range of e keeps it
+ * a normal bf16 number), and lets the tensor cores apply the scales.  A block
+ * that holds an infinity or a NaN has scale 255 and is NaN throughout, so an
+ * overflow is never hidden by a saturated code.
+ *
+ * rows, cols, n, k >= 0 (else SLIM_ERR_INVALID_ARG).  A call with nothing to
+ * write is a no-op.  Entry points take bf16 rows, or fp32 ones with _f32;
+ * rows are dense row-major.  Misaligned codes, scales or workspaces, and
+ * matrices of 2^31 or more blocks, return SLIM_ERR_UNSUPPORTED.  Arithmetic is
+ * fp32; every call only enqueues work on `stream` and allocates nothing. */
+
+/* Bytes of the two buffers of an 8-bit matrix; R = block_rows, 1 or 128.
+ * 0 for an empty matrix or an invalid argument. */
+size_t slim_q8_codes_bytes(int rows, int cols);
+size_t slim_q8_scales_bytes(int rows, int cols, int block_rows);
+
+/* x [rows][cols] into codes and scales (R = 1). */
+slim_status slim_q8_quantize(const void *x, void *codes, void *scales, int rows, int cols, slim_stream_t stream);
+slim_status slim_q8_quantize_f32(const float *x, void *codes, void *scales, int rows, int cols,
+                                 slim_stream_t stream);
+
+/* The values of an 8-bit matrix, block_rows = 1 or 128. */
+slim_status slim_q8_dequantize(const void *codes, const void *scales, void *x, int rows, int cols, int block_rows,
+                               slim_stream_t stream);
+slim_status slim_q8_dequantize_f32(const void *codes, const void *scales, float *x, int rows, int cols,
+                                   int block_rows, slim_stream_t stream);
+
+/* A weight w [n][k] with one scale for each 128 x 128 block (R = 128), and,
+ * where codes_t and scales_t are not NULL, its transpose [k][n] with the same
+ * codes and scales, for the data gradient. */
+slim_status slim_q8_pack_weight(const void *w, void *codes, void *scales, void *codes_t, void *scales_t, int n,
+                                int k, slim_stream_t stream);
+slim_status slim_q8_pack_weight_f32(const float *w, void *codes, void *scales, void *codes_t, void *scales_t, int n,
+                                    int k, slim_stream_t stream);
+
+/* Root-mean-square norm with the residual's addition:
+ *   h = x + res (rounded to the I/O type; x itself where res is NULL),
+ *   rstd = 1 / sqrt(mean over cols of h^2 + eps),
+ *   y = 8 bits of h * rstd * gamma (R = 1).
+ * h: NULL, or [rows][cols] (may be x or res).  rstd: NULL, or fp32 [rows].
+ * gamma: fp32 [cols].  h_codes, h_scales: NULL, or the 8-bit checkpoint of h
+ * for the backward.  1 <= cols <= 16384, else SLIM_ERR_INVALID_ARG or
+ * SLIM_ERR_UNSUPPORTED; eps >= 0. */
+slim_status slim_q8_rms_norm(const void *x, const void *res, const float *gamma, float eps, void *h, float *rstd,
+                             void *y_codes, void *y_scales, void *h_codes, void *h_scales, int rows, int cols,
+                             slim_stream_t stream);
+slim_status slim_q8_rms_norm_f32(const float *x, const float *res, const float *gamma, float eps, float *h,
+                                 float *rstd, void *y_codes, void *y_scales, void *h_codes, void *h_scales, int rows,
+                                 int cols, slim_stream_t stream);
+
+/* Its gradients.  dy: the gradient at the norm's output (the rounding to 8
+ * bits passes it through); the kept rows are h in full, or its checkpoint
+ * h_codes, h_scales (exactly one of the two); dres: NULL, or the gradient
+ * that reaches h by other ways (the residual stream).  With n = h * rstd,
+ * g = dy * gamma:
+ *   dh = rstd * (g - n * mean(g * n)) + dres, the gradient of x and of res
+ *   (may be dy or dres);
+ *   dgamma[c] = sum over rows of dy * n: fp32 [cols], overwritten, summed in
+ *   an order that depends on the shape alone; or NULL.
+ * workspace: 16-byte aligned device memory of
+ * slim_q8_rms_norm_bwd_workspace_bytes (needed for dgamma only). */
+slim_status slim_q8_rms_norm_bwd(const void *dy, const void *h, const void *h_codes, const void *h_scales,
+                                 const float *rstd, const float *gamma, const void *dres, void *dh, float *dgamma,
+                                 void *workspace, size_t workspace_bytes, int rows, int cols, slim_stream_t stream);
+slim_status slim_q8_rms_norm_bwd_f32(const float *dy, const float *h, const void *h_codes, const void *h_scales,
+                                     const float *rstd, const float *gamma, const float *dres, float *dh,
+                                     float *dgamma, void *workspace, size_t workspace_bytes, int rows, int cols,
+                                     slim_stream_t stream);
+size_t slim_q8_rms_norm_bwd_workspace_bytes(int rows, int cols);
+
+/* a = 8 bits of GeLU(z) = z Phi(z) (exact normal distribution function), and,
+ * where z_codes and z_scales are not NULL, the 8-bit checkpoint of z. */
+slim_status slim_q8_gelu(const void *z, void *a_codes, void *a_scales, void *z_codes, void *z_scales, int rows,
+                         int cols, slim_stream_t stream);
+slim_status slim_q8_gelu_f32(const float *z, void *a_codes, void *a_scales, void *z_codes, void *z_scales, int rows,
+                             int cols, slim_stream_t stream);
+
+/* dz = da * (Phi(z) + z phi(z)) at the checkpointed z.  dz may be da.
+ * dz_codes, dz_scales: NULL, or the 8 bits of dz as slim_q8_quantize gives
+ * them (the operand of the data gradient), from the same pass. */
+slim_status slim_q8_gelu_bwd(const void *da, const void *z_codes, const void *z_scales, void *dz, void *dz_codes,
+                             void *dz_scales, int rows, int cols, slim_stream_t stream);
+slim_status slim_q8_gelu_bwd_f32(const float *da, const void *z_codes, const void *z_scales, float *dz,
+                                 void *dz_codes, void *dz_scales, int rows, int cols, slim_stream_t stream);
+
+/* out [rows][n] = a [rows][k] . b [n][k]^T: a with R = 1, b a packed weight
+ * (R = 128).  Products and sums in fp32 on the tensor cores (tcgen05, scales
+ * applied per 128 columns), rounded once to out.  Rows past `rows` and columns
+ * past n of the buffers are never read or written.  k = 0 gives zeros.
+ * Data gradient: a = 8 bits of dY, b = the transposed packed weight. */
+slim_status slim_q8_matmul(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales,
+                           void *out, int rows, int n, int k, slim_stream_t stream);
+slim_status slim_q8_matmul_f32(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales,
+                               float *out, int rows, int n, int k, slim_stream_t stream);
+
+/* Weight gradient from the 8-bit checkpoint of the product's input:
+ * dw [n][k] (fp32) = sum over rows of dy[row][n] * x[row][k], added to dw
+ * where accumulate is not 0.  dy: bf16 [rows][n]; x: R = 1.  Products of the
+ * bf16 dy and the (exactly bf16) values of x, summed in fp32 in an order that
+ * depends on the shape and the device's SM count alone.  workspace: 16-byte
+ * aligned device memory of slim_q8_wgrad_workspace_bytes(rows, n, k) bytes
+ * (NULL where that is 0). */
+slim_status slim_q8_wgrad(const void *dy, const void *x_codes, const void *x_scales, float *dw, int accumulate,
+                          void *workspace, size_t workspace_bytes, int rows, int n, int k, slim_stream_t stream);
+size_t slim_q8_wgrad_workspace_bytes(int rows, int n, int k);
+
 /* Bytes of workspace slim_attn_fwd (is_bwd = 0) or slim_attn_bwd (is_bwd = 1)
  * need for this shape on the current device (either I/O type).  0 for an
  * unsupported shape or an empty problem. */

@@ -107,6 +107,12 @@ EXPORTED = (
     "slim_attn_fwd_carry", "slim_attn_bwd_carry", "slim_attn_fwd_carry_f32", "slim_attn_bwd_carry_f32",
     "slim_attn_copy_rows", "slim_attn_draw_orf", "slim_lm_param_count", "slim_lm_workspace_bytes",
     "slim_lm_loss_grad", "slim_lm_checkpoint_bytes", "slim_attn_probe_ex2",
+    "slim_q8_codes_bytes", "slim_q8_scales_bytes", "slim_q8_quantize", "slim_q8_quantize_f32",
+    "slim_q8_dequantize", "slim_q8_dequantize_f32", "slim_q8_pack_weight", "slim_q8_pack_weight_f32",
+    "slim_q8_rms_norm", "slim_q8_rms_norm_f32", "slim_q8_rms_norm_bwd", "slim_q8_rms_norm_bwd_f32",
+    "slim_q8_rms_norm_bwd_workspace_bytes", "slim_q8_gelu", "slim_q8_gelu_f32", "slim_q8_gelu_bwd",
+    "slim_q8_gelu_bwd_f32", "slim_q8_matmul", "slim_q8_matmul_f32", "slim_q8_wgrad",
+    "slim_q8_wgrad_workspace_bytes",
 )
 
 

@@ -1,0 +1,56 @@
+// q8_tc.cuh -- tensor-core and TMA pieces of the 8-bit products.
+#pragma once
+
+#include "q8_common.cuh"
+#include "tc_common.cuh"
+
+namespace slim {
+namespace q8 {
+
+using namespace tc;
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Instruction descriptor, kind::mxf8f6f4 with e4m3 A and B, fp32 D and E8M0
+// scales, one for each row and 32 columns of an operand: the byte a_sf (b_sf)
+// of a row's 32-bit scale word.
+//   bits 4-5 B scale byte, 7-9 / 10-12 A / B format (0 = e4m3),
+//   17-22 N >> 3, 23 scale format (1 = E8M0), 24-28 M >> 4, 29-30 A scale byte.
+__device__ __forceinline__ uint32_t make_idesc_mx8(uint32_t M, uint32_t N, uint32_t sf) {
+  return (sf << 4) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) | (sf << 29);
+}
+
+// D[tmem] (+)= (A * 2^sa) (B * 2^sb)^T over 32 columns, issued by one thread.
+// Scale words: row r of an operand is TMEM lane r % 32 of column r / 32 from
+// the given address, the same in each of the four 32-lane groups.
+__device__ __forceinline__ void mma_mx8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Four 32-bit columns into this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st4u(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+}  // namespace q8
+}  // namespace slim
