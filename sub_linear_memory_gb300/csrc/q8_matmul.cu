@@ -214,10 +214,288 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
 }
 
 }  // namespace sm
+
+// ---- many output tiles: a CTA pair for each 256 x NT tile --------------------------
+//
+// Two SMs work on one tile (cta_group::2), each loads half of either operand,
+// so a 128-byte step of k moves 32 KB into each SM's shared memory for 512
+// cycles of MMA.  Pairs walk the tiles; one warp loads, one thread of the pair
+// issues, four warps put the scale words into tensor memory (512 columns of k
+// at a time), four warps turn the finished accumulator into rows of out while
+// the next tile is multiplied into the other one.
+namespace lg {
+
+constexpr int kThreads = 384, kStages = 6, kTm = 256;
+constexpr uint32_t kA = kBlock * kBlock;
+constexpr uint32_t kOut = 4096;  // one warp's 32 rows x 128 bytes of out
+enum {
+  S_FULL = 0, S_EMPTY = S_FULL + kStages, S_SF = S_EMPTY + kStages, S_SFFREE = S_SF + 2, S_ACC = S_SFFREE + 2,
+  S_ACCFREE = S_ACC + 2, S_DONE, S_COUNT
+};
+
+template <int NT> struct Lay {
+  static constexpr uint32_t kB = NT / 2 * kBlock, kStage = kA + kB;
+  static constexpr uint32_t kOutAt = kStages * kStage, kBar = kOutAt + 8 * kOut, kSmem = 1024 + kBar + 256;
+  // Tensor memory: two accumulators, and two sets of 12 scale columns at the
+  // end.  Two of 256 columns do not fit beside them, so they share 32 columns,
+  // which the epilogue reads first.
+  static constexpr uint32_t kSf = 480;
+  static constexpr bool kOverlap = 2 * NT > 480;
+  static constexpr uint32_t kAcc1 = kOverlap ? 480 - NT : NT;
+};
+
+template <int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                  const __grid_constant__ CUtensorMap mo, const uint8_t *a_scales, const uint8_t *b_scales, void *out,
+                  int rows, int n, int kb, int pitch, int tiles_n, int tiles, int tma_out, int *status) {
+  using LY = Lay<NT>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t sbase = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t *smem = raw + (sbase - smem_u32(raw));
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + LY::kBar);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + S_COUNT);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar + S_FULL + s, 1);
+      mbar_init(bar + S_EMPTY + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar + S_SF + b, 8);  // four warps of each CTA
+      mbar_init(bar + S_SFFREE + b, 1);
+      mbar_init(bar + S_ACC + b, 1);
+    }
+    mbar_init(bar + S_ACCFREE, 8);
+    mbar_init(bar + S_DONE, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&ma);
+    prefetch_tmap(&mb);
+    if (tma_out) prefetch_tmap(&mo);
+  }
+  if (warp == 2) tmem_alloc_pair(tslot, 512);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  bool ok = true;
+  auto wait = [&](int b, uint32_t par) {
+    if (ok) ok = mbar_wait(bar + b, par, status, abort_flag);
+    return ok;
+  };
+  auto wait_pair = [&](int b, uint32_t par) {  // where threads of both CTAs arrive
+    if (ok) ok = mbar_wait_cluster(bar + b, par, status, abort_flag);
+    return ok;
+  };
+  // arrive on the leading CTA's barrier, once for the warp
+  auto arrive_leader = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(map_peer(smem_u32(bar + b), 0));
+  };
+
+  if (warp == 0 && lane == 0) {
+    int i = 0;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * NT + (int)rank * (NT / 2);
+      for (int kk = 0; kk < kb; ++kk, ++i) {
+        const int s = i % kStages;
+        if (i >= kStages && !wait(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1)) break;
+        if (rank == 0) mbar_arrive_expect_tx(bar + S_FULL + s, 2 * LY::kStage);
+        const uint32_t full = map_peer(smem_u32(bar + S_FULL + s), 0), at = sbase + s * LY::kStage;
+        tma_load_2d_pair(at, &ma, full, kk * kBlock, m0);
+        tma_load_2d_pair(at + kA, &mb, full, kk * kBlock, n0);
+      }
+    }
+    if (rank == 0)
+      for (int j = max(0, i - kStages); j < i; ++j) mbar_drain(bar + S_FULL + j % kStages, (uint32_t)(j / kStages) & 1);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    int i = 0, quad = 0, j = 0;
+    for (int t = pair; t < tiles && ok; t += pairs, ++j) {
+      // the accumulator's columns are free: those it shares with the last
+      // tile's have been read, or all of the tile's before that
+      if (LY::kOverlap ? j > 0 && !wait_pair(S_ACCFREE, (uint32_t)(j - 1) & 1)
+                       : j > 1 && !wait_pair(S_ACCFREE, (uint32_t)(j - 2) & 1))
+        break;
+      tc_fence_after();
+      const uint32_t acc = tbase + (j & 1 ? LY::kAcc1 : 0);
+      for (int kk = 0; kk < kb; ++kk, ++i) {
+        const uint32_t sf = tbase + LY::kSf + 12 * (quad & 1);
+        if ((kk & 3) == 0 && !wait_pair(S_SF + (quad & 1), (uint32_t)(quad >> 1) & 1)) break;
+        const int s = i % kStages;
+        if (!wait(S_FULL + s, (uint32_t)(i / kStages) & 1)) break;
+        tc_fence_after();
+        const uint32_t id = make_idesc_mx8(kTm, NT, kk & 3);
+        const uint64_t da = make_desc(sbase + s * LY::kStage, 16u, 1024u, kSwizzle128);
+        const uint64_t db = make_desc(sbase + s * LY::kStage + kA, 16u, 1024u, kSwizzle128);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mma_mx8_pair(acc, da + 2 * x, db + 2 * x, id, sf, sf + 4, kk > 0 || x > 0);
+        mma_commit_pair(bar + S_EMPTY + s);
+        if ((kk & 3) == 3 || kk == kb - 1) {
+          mma_commit_pair(bar + S_SFFREE + (quad & 1));
+          ++quad;
+        }
+      }
+      if (ok) mma_commit_pair(bar + S_ACC + (j & 1));
+    }
+    mma_commit_pair(bar + S_DONE);
+    mbar_drain(bar + S_DONE, 0);
+  } else if (warp >= 4 && warp < 8) {
+    // scale words of 4 blocks of k at a time: 128 rows of a (this CTA's), NT rows of b
+    const uint32_t at0 = tmem_addr(tbase, 32u * (warp & 3), LY::kSf);
+    constexpr uint32_t kOnes = 0x7f7f7f7fu;
+    int quad = 0;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * NT;
+      for (int kk = 0; kk < kb; kk += 4, ++quad) {
+        uint32_t a[4], b[8];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int m = m0 + 32 * g + lane;
+          a[g] = m < rows ? __ldg(reinterpret_cast<const uint32_t *>(a_scales + (size_t)m * pitch + kk)) : kOnes;
+        }
+#pragma unroll
+        for (int g = 0; g < NT / 32; ++g) {
+          const int nn = n0 + 32 * g;
+          b[g] = nn < n ? __ldg(reinterpret_cast<const uint32_t *>(b_scales + (size_t)(nn / kBlock) * pitch + kk)) : kOnes;
+        }
+#pragma unroll
+        for (int g = NT / 32; g < 8; ++g) b[g] = kOnes;
+        if (quad >= 2 && !wait(S_SFFREE + (quad & 1), (uint32_t)((quad >> 1) - 1) & 1)) break;
+        tc_fence_after();
+        const uint32_t at = at0 + 12 * (quad & 1);
+        __syncwarp();
+        tmem_st4u(at, a[0], a[1], a[2], a[3]);
+        tmem_st4u(at + 4, b[0], b[1], b[2], b[3]);
+        tmem_st4u(at + 8, b[4], b[5], b[6], b[7]);
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_leader(S_SF + (quad & 1));
+      }
+    }
+  } else if (warp >= 8) {
+    const int w = warp - 8;
+    const uint32_t lanes = 32u * w;
+    constexpr int kCols = F32 ? 32 : 64;  // 128 bytes of a row of out
+    constexpr int kChunks = NT / kCols;
+    int j = 0, turn = 0;
+    for (int t = pair; t < tiles && ok; t += pairs, ++j) {
+      const int m0 = t / tiles_n * kTm + (int)rank * kBlock + 32 * w, n0 = t % tiles_n * NT;
+      if (!wait(S_ACC + (j & 1), (uint32_t)(j >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t acc = j & 1 ? LY::kAcc1 : 0;
+      for (int x = 0; x < kChunks; ++x) {
+        // the columns shared with the other accumulator first: the last of the first, the first of the second
+        const int c = (LY::kOverlap && !(j & 1) ? kChunks - 1 - x : x) * kCols;
+        float v[kCols];
+        __syncwarp();
+        if constexpr (F32) tmem_ld32(tmem_addr(tbase, lanes, acc + c), v);
+        else tmem_ld32x2(tmem_addr(tbase, lanes, acc + c), tmem_addr(tbase, lanes, acc + c + 32), v, v + 32);
+        if (x == (LY::kOverlap ? 0 : kChunks - 1)) {
+          tc_fence_before();
+          arrive_leader(S_ACCFREE);
+        }
+        if (m0 >= rows || n0 + c >= n) continue;  // uniform over the warp
+        const uint32_t buf = sbase + LY::kOutAt + (2 * w + (turn & 1)) * kOut;
+        ++turn;
+        // the store that last read this buffer is done reading
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t to = buf + lane * 128u + ((uint32_t)(q ^ (lane & 7)) << 4);
+          if constexpr (F32)
+            st_shared_v4(to, __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                         __float_as_uint(v[4 * q + 3]));
+          else
+            st_bf16x8(to, v + 8 * q);
+        }
+        if (tma_out) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&mo, buf, n0 + c, m0);
+            tma_store_commit();
+          }
+        } else {  // rows of out that do not start on 16 bytes: coalesced stores of single elements
+          __syncwarp();
+          const int live = min(32, rows - m0), left = n - n0 - c;
+          for (int r = 0; r < live; ++r) {
+#pragma unroll
+            for (int h = 0; h < kCols / 32; ++h) {
+              const int col = lane + 32 * h;
+              const uint32_t bytes = (uint32_t)col * (128 / kCols);
+              const uint8_t *from = smem + (buf - sbase) + r * 128 + (((bytes >> 4) ^ (r & 7)) << 4) + (bytes & 15);
+              const size_t to = (size_t)(m0 + r) * n + n0 + c + col;
+              if (col < left) {
+                if constexpr (F32) static_cast<float *>(out)[to] = *reinterpret_cast<const float *>(from);
+                else static_cast<__nv_bfloat16 *>(out)[to] = *reinterpret_cast<const __nv_bfloat16 *>(from);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) tma_store_wait_all();
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp == 2) tmem_dealloc_pair(tbase, 512);
+}
+
+template <int NT, bool F32>
+cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
+                   int rows, int n, int k, int *status, cudaStream_t st) {
+  using LY = Lay<NT>;
+  constexpr int kSize = F32 ? 4 : 2;
+  const int kb = blocks_of(k), tiles_n = (n + NT - 1) / NT;
+  const long long tiles = (((long long)rows + kTm - 1) / kTm) * tiles_n;
+  const uint64_t kp = (uint64_t)kb * kBlock;
+  const bool tma_out = (long long)n * kSize % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  CUtensorMap ma, mb, mo;
+  if (!make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, rows, kp, kp, kBlock, kBlock, true) ||
+      !make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, n, kp, kp, NT / 2, kBlock, true))
+    return cudaErrorInvalidValue;
+  mo = ma;
+  if (tma_out && !make_map_2d(&mo, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, rows,
+                              n, (uint64_t)n * kSize, 32, 128 / kSize, true))
+    return cudaErrorInvalidValue;
+  auto kern = matmul_kernel<NT, F32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(152, 2 * tiles));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = LY::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope ps("q8_matmul", st);
+  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, static_cast<const uint8_t *>(a_scales),
+                         static_cast<const uint8_t *>(b_scales), out, rows, n, kb, scale_pitch(k), tiles_n, (int)tiles,
+                         tma_out ? 1 : 0, status);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace lg
 }  // namespace
 
 cudaError_t matmul(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                    bool f32, int rows, int n, int k, int *status, cudaStream_t st) {
+  const long long tiles = (long long)((rows + 255) / 256) * ((n + 255) / 256);
+  if (tiles >= 38) {
+    return f32 ? lg::launch<256, true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
+               : lg::launch<256, false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
+  }
   return f32 ? sm::launch<true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
              : sm::launch<false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
 }

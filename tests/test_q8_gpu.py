@@ -299,10 +299,21 @@ def test_matmul(q8, rows, n, k, dtype):
     assert torch.equal(q8.matmul(a, w, dtype=dtype), out)
 
 
-def test_matmul_scales_of_every_block(q8):
+# output tiles enough for the persistent kernel: ragged in each direction, rows of
+# out on and off 16 bytes, one block of k to many
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows, n, k", [(2560, 1024, 1024), (9728, 256, 128), (2433, 1033, 700), (1300, 2056, 392),
+                                        (5000, 520, 1928), (257, 9999, 264), (12000, 1001, 136), (3000, 1536, 4000)])
+def test_matmul_many_tiles(q8, rows, n, k, dtype):
+    a, w = pair(q8, rows, n, k, 2)
+    out = check_matmul(q8, a, w, dtype)
+    assert torch.equal(q8.matmul(a, w, dtype=dtype), out)
+
+
+@pytest.mark.parametrize("rows, n, k", [(130, 260, 1300), (2433, 1033, 1300)])
+def test_matmul_scales_of_every_block(q8, rows, n, k):
     """Blocks whose scales differ by many powers of two, in both operands, and
     one block alone deciding each result (an exact product)."""
-    rows, n, k = 130, 260, 1300
     a = torch.zeros((rows, k))
     w = torch.zeros((n, k))
     r, c = torch.arange(rows), torch.arange(n)
@@ -334,8 +345,8 @@ def test_matmul_nan_and_empty(q8):
     assert q8.matmul(q8.quantize(draw((0, 64), 1)), q8.pack_weight(draw((6, 64), 1))[0]).shape == (0, 6)
 
 
-def test_matmul_writes_inside_its_output_only(q8):
-    rows, n, k = 131, 203, 260
+@pytest.mark.parametrize("rows, n, k", [(131, 203, 260), (2433, 1035, 260), (2433, 1040, 260)])
+def test_matmul_writes_inside_its_output_only(q8, rows, n, k):
     a, w = pair(q8, rows, n, k, 1)
     for dtype in (BF16, F32):
         buf = torch.full((rows * n + 512,), 7.0, dtype=dtype, device="cuda")
