@@ -234,6 +234,7 @@ enum {
 };
 
 template <int NT> struct Lay {
+  static_assert(NT % kBlock == 0, "a tile's columns are whole blocks of the weight's scales");
   static constexpr uint32_t kB = NT / 2 * kBlock, kStage = kA + kB;
   static constexpr uint32_t kOutAt = kStages * kStage, kBar = kOutAt + 8 * kOut, kSmem = 1024 + kBar + 256;
   // Tensor memory: two accumulators, and two sets of 12 scale columns at the
@@ -287,9 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) ok = mbar_wait(bar + b, par, status, abort_flag);
     return ok;
   };
-  auto wait_pair = [&](int b, uint32_t par) {  // where threads of both CTAs arrive
-    if (ok) ok = mbar_wait_cluster(bar + b, par, status, abort_flag);
-    return ok;
+  auto wait_warp = [&](int b, uint32_t par) {  // called by a whole warp, whose lanes agree on the result
+    wait(b, par);
+    return ok = __all_sync(0xffffffffu, ok);
   };
   // arrive on the leading CTA's barrier, once for the warp
   auto arrive_leader = [&](int b) {
@@ -312,65 +313,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (rank == 0)
       for (int j = max(0, i - kStages); j < i; ++j) mbar_drain(bar + S_FULL + j % kStages, (uint32_t)(j / kStages) & 1);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
+    const bool issues = elect_lane();
     int i = 0, quad = 0, j = 0;
     for (int t = pair; t < tiles && ok; t += pairs, ++j) {
       // the accumulator's columns are free: those it shares with the last
       // tile's have been read, or all of the tile's before that
-      if (LY::kOverlap ? j > 0 && !wait_pair(S_ACCFREE, (uint32_t)(j - 1) & 1)
-                       : j > 1 && !wait_pair(S_ACCFREE, (uint32_t)(j - 2) & 1))
+      if (LY::kOverlap ? j > 0 && !wait_warp(S_ACCFREE, (uint32_t)(j - 1) & 1)
+                       : j > 1 && !wait_warp(S_ACCFREE, (uint32_t)(j - 2) & 1))
         break;
       tc_fence_after();
       const uint32_t acc = tbase + (j & 1 ? LY::kAcc1 : 0);
       for (int kk = 0; kk < kb; ++kk, ++i) {
         const uint32_t sf = tbase + LY::kSf + 12 * (quad & 1);
-        if ((kk & 3) == 0 && !wait_pair(S_SF + (quad & 1), (uint32_t)(quad >> 1) & 1)) break;
+        if ((kk & 3) == 0 && !wait_warp(S_SF + (quad & 1), (uint32_t)(quad >> 1) & 1)) break;
         const int s = i % kStages;
-        if (!wait(S_FULL + s, (uint32_t)(i / kStages) & 1)) break;
+        if (!wait_warp(S_FULL + s, (uint32_t)(i / kStages) & 1)) break;
         tc_fence_after();
         const uint32_t id = make_idesc_mx8(kTm, NT, kk & 3);
         const uint64_t da = make_desc(sbase + s * LY::kStage, 16u, 1024u, kSwizzle128);
         const uint64_t db = make_desc(sbase + s * LY::kStage + kA, 16u, 1024u, kSwizzle128);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) mma_mx8_pair(acc, da + 2 * x, db + 2 * x, id, sf, sf + 4, kk > 0 || x > 0);
-        mma_commit_pair(bar + S_EMPTY + s);
+        for (int x = 0; x < 4; ++x)
+          if (issues) mma_mx8_pair(acc, da + 2 * x, db + 2 * x, id, sf, sf + 4, kk > 0 || x > 0);
+        if (issues) mma_commit_pair(bar + S_EMPTY + s);
         if ((kk & 3) == 3 || kk == kb - 1) {
-          mma_commit_pair(bar + S_SFFREE + (quad & 1));
+          if (issues) mma_commit_pair(bar + S_SFFREE + (quad & 1));
           ++quad;
         }
+        __syncwarp();
       }
-      if (ok) mma_commit_pair(bar + S_ACC + (j & 1));
+      if (ok && issues) mma_commit_pair(bar + S_ACC + (j & 1));
+      __syncwarp();
     }
-    mma_commit_pair(bar + S_DONE);
+    if (issues) mma_commit_pair(bar + S_DONE);
+    __syncwarp();
     mbar_drain(bar + S_DONE, 0);
   } else if (warp >= 4 && warp < 8) {
-    // scale words of 4 blocks of k at a time: 128 rows of a (this CTA's), NT rows of b
+    // scale words of 4 blocks of k at a time: 128 rows of a (this CTA's), NT
+    // rows of b.  The words of the next 4 blocks (of the next tile, at the end
+    // of one) are on their way from memory while these wait for their columns:
+    // loaded only then, they held up the MMAs (2.19 -> XX PFLOP/s).
     const uint32_t at0 = tmem_addr(tbase, 32u * (warp & 3), LY::kSf);
     constexpr uint32_t kOnes = 0x7f7f7f7fu;
-    int quad = 0;
-    for (int t = pair; t < tiles && ok; t += pairs) {
+    struct Words {
+      uint32_t a[4], b[(NT + kBlock - 1) / kBlock];
+    };
+    auto fetch = [&](int t, int kk, Words &w) {
       const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * NT;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int m = m0 + 32 * g + lane;
+        w.a[g] = m < rows ? __ldg(reinterpret_cast<const uint32_t *>(a_scales + (size_t)m * pitch + kk)) : kOnes;
+      }
+#pragma unroll
+      for (int g = 0; g < (NT + kBlock - 1) / kBlock; ++g) {
+        const int blk = n0 / kBlock + g;
+        w.b[g] = blk * kBlock < n ? __ldg(reinterpret_cast<const uint32_t *>(b_scales + (size_t)blk * pitch + kk)) : kOnes;
+      }
+    };
+    int quad = 0;
+    Words now, next;
+    if (pair < tiles) fetch(pair, 0, next);
+    for (int t = pair; t < tiles && ok; t += pairs) {
       for (int kk = 0; kk < kb; kk += 4, ++quad) {
-        uint32_t a[4], b[8];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int m = m0 + 32 * g + lane;
-          a[g] = m < rows ? __ldg(reinterpret_cast<const uint32_t *>(a_scales + (size_t)m * pitch + kk)) : kOnes;
-        }
-#pragma unroll
-        for (int g = 0; g < NT / 32; ++g) {
-          const int nn = n0 + 32 * g;
-          b[g] = nn < n ? __ldg(reinterpret_cast<const uint32_t *>(b_scales + (size_t)(nn / kBlock) * pitch + kk)) : kOnes;
-        }
-#pragma unroll
-        for (int g = NT / 32; g < 8; ++g) b[g] = kOnes;
+        now = next;
+        if (kk + 4 < kb) fetch(t, kk + 4, next);
+        else if (t + pairs < tiles) fetch(t + pairs, 0, next);
         if (quad >= 2 && !wait(S_SFFREE + (quad & 1), (uint32_t)((quad >> 1) - 1) & 1)) break;
         tc_fence_after();
         const uint32_t at = at0 + 12 * (quad & 1);
+        const uint32_t b0 = now.b[0], b1 = now.b[(NT - 1) / kBlock];
         __syncwarp();
-        tmem_st4u(at, a[0], a[1], a[2], a[3]);
-        tmem_st4u(at + 4, b[0], b[1], b[2], b[3]);
-        tmem_st4u(at + 8, b[4], b[5], b[6], b[7]);
+        tmem_st4u(at, now.a[0], now.a[1], now.a[2], now.a[3]);
+        tmem_st4u(at + 4, b0, b0, b0, b0);
+        tmem_st4u(at + 8, b1, b1, b1, b1);
         tmem_st_wait();
         tc_fence_before();
         arrive_leader(S_SF + (quad & 1));

@@ -17,6 +17,20 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// True in one lane of a converged warp.  A warp whose lanes run the issuing
+// loop together and leave only the tcgen05 instructions to that lane keeps the
+// loop's addresses and descriptors in uniform registers; a loop run by one
+// lane alone spent more time forming them than the MMAs took.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Instruction descriptor, kind::mxf8f6f4 with e4m3 A and B, fp32 D and E8M0
 // scales, one for each row and 32 columns of an operand: the byte a_sf (b_sf)
 // of a row's 32-bit scale word.
@@ -81,25 +95,6 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
-}
-
-// mbar_wait for a barrier that threads of the other CTA arrive on: what they
-// wrote before it is seen after it.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, int *status, volatile int *abort) {
-  auto ready = [&] {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-  };
-  if (ready()) return true;
-  if (!mbar_wait(bar, parity, status, abort)) return false;
-  return ready();  // complete: acquires
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
