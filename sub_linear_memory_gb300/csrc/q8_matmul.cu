@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scale words of 4 blocks of k at a time: 128 rows of a (this CTA's), NT
     // rows of b.  The words of the next 4 blocks (of the next tile, at the end
     // of one) are on their way from memory while these wait for their columns:
-    // loaded only then, they held up the MMAs (2.19 -> XX PFLOP/s).
+    // loaded only then, a first load from DRAM would hold up the MMAs.
     const uint32_t at0 = tmem_addr(tbase, 32u * (warp & 3), LY::kSf);
     constexpr uint32_t kOnes = 0x7f7f7f7fu;
     struct Words {

@@ -303,7 +303,8 @@ def test_matmul(q8, rows, n, k, dtype):
 # out on and off 16 bytes, one block of k to many
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows, n, k", [(2560, 1024, 1024), (9728, 256, 128), (2433, 1033, 700), (1300, 2056, 392),
-                                        (5000, 520, 1928), (257, 9999, 264), (12000, 1001, 136), (3000, 1536, 4000)])
+                                        (5000, 520, 1928), (257, 9999, 264), (12000, 1001, 136), (3000, 1536, 4000),
+                                        (20001, 1033, 520), (40000, 640, 1160)])
 def test_matmul_many_tiles(q8, rows, n, k, dtype):
     a, w = pair(q8, rows, n, k, 2)
     out = check_matmul(q8, a, w, dtype)
