@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // arrive on the leading CTA's barrier, once for the warp
   auto arrive_leader = [&](int b) {
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(map_peer(smem_u32(bar + b), 0));
+    if (lane == 0) mbar_arrive_pair(map_peer(smem_u32(bar + b), 0));
   };
 
   if (warp == 0 && lane == 0) {

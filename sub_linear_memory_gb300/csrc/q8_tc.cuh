@@ -88,6 +88,34 @@ __device__ __forceinline__ void mma_mx8_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on a barrier of either CTA of the pair (cluster address).  What the
+// barrier hands over here is read by the tensor cores of the SM it was written
+// on (shared memory after fence.proxy.async, tensor memory after
+// tcgen05.wait), so the arrival needs no ordering of memory across the
+// cluster; arriving with release at cluster scope instead made every
+// converting warp wait for its stores (a weight gradient took 1072 us, not 612).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t rbar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(rbar) : "memory");
+}
+
+// Registers of this warpgroup (all four warps call).
+template <int N> __device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Arrive on the barrier at this offset in both CTAs once every MMA issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
   asm volatile(

@@ -3,15 +3,27 @@
 //
 // The sum runs over rows, across which the scales of x differ, so the tensor
 // cores cannot apply them; but code * 2^e is exactly a bf16 number, and dy is
-// bf16.  Eight warps turn each tile of codes into bf16 in shared memory (a
+// bf16.  Four warps turn each tile of codes into bf16 in shared memory (a
 // shift, two masks and one packed multiply for two codes) while the tensor
-// cores (kind::f16, both operands MN-major) work on the tile before.
+// cores (kind::f16, both operands MN-major) work on the tiles before.
 //
-// Split: an output tile is 128 (n) x 256 (k), and the rows are cut into steps
-// of 64.  All steps of all tiles form one line that is cut evenly over the
-// CTAs, so every SM has the same share whatever the shape; a CTA that does not
-// hold all steps of a tile leaves a partial tile in the workspace, and a
-// second kernel adds the partials in the order of the line.
+// Tile: a CTA pair (cta_group::2) forms 256 (n) x 256 (k), each CTA loading
+// 128 columns of dy and converting one 128-column block of x, so that a code
+// is converted once for 256 results.  With one CTA for 128 x 256 the
+// conversion and the shared memory it passes through took four times the
+// MMAs' time.
+//
+// Rounding: the tensor cores add into their fp32 accumulator with truncation;
+// over the 4096 additions of 65536 rows that lost 4e-5 of the result.  The
+// accumulator is therefore emptied every 20 steps (80 additions) into
+// registers of eight other warps, which add with rounding to nearest, while
+// the MMAs go on in a second accumulator.
+//
+// Split: the rows are cut into steps of 64, and all steps of all tiles form
+// one line that is cut evenly over the pairs, so every SM has the same share
+// whatever the shape; a pair that does not hold all steps of a tile leaves a
+// partial tile in the workspace, and a second kernel adds the partials in the
+// order of the line.
 #include <algorithm>
 
 #include "kernels.h"
@@ -23,25 +35,28 @@ namespace slim {
 namespace q8 {
 namespace {
 
-constexpr int kCtas = 152;      // one per SM
-constexpr int kTn = 128, kTk = 256, kStep = 64;
-constexpr int kMinSteps = 4;    // per CTA: a partial tile costs about this much
-constexpr int kThreads = 384;   // producer, MMA, two idle, eight converting warps
-constexpr int kStages = 4;
-constexpr uint32_t kABytes = kStep * kTn * 2, kCBytes = kStep * kTk, kBBytes = kStep * kTk * 2;
-constexpr uint32_t kStageBytes = kABytes + kCBytes;
+constexpr int kPairs = 76;      // one CTA for each of 152 SMs
+constexpr int kTn = 256, kTk = 256, kStep = 64;  // a pair's tile and rows of a step
+constexpr int kMinSteps = 8;    // per pair: a partial tile costs about this much
+constexpr int kWindow = 20;     // steps in one accumulator
+constexpr int kThreads = 512;   // loads, MMA, tensor memory, scales; four converting, eight adding warps
+constexpr int kStages = 6, kBufs = 4;
+constexpr uint32_t kDBytes = kStep * kBlock * 2, kCBytes = kStep * kBlock, kBBytes = kStep * kBlock * 2;
+constexpr uint32_t kStageBytes = kDBytes + kCBytes;
+constexpr uint32_t kTable = kStep * 8;  // factors of a step's rows
+constexpr uint32_t oB = kStages * kStageBytes, oTable = oB + kBufs * kBBytes, oBar = oTable + kStages * kTable;
 enum {
-  S_FULL = 0, S_EMPTY = S_FULL + kStages, S_BFULL = S_EMPTY + kStages, S_BEMPTY = S_BFULL + 2, S_ACC = S_BEMPTY + 2,
-  S_ACCFREE, S_COUNT
+  S_DY = 0, S_CODES = S_DY + kStages, S_EMPTY = S_CODES + kStages, S_BFULL = S_EMPTY + kStages,
+  S_BEMPTY = S_BFULL + kBufs, S_ACC = S_BEMPTY + kBufs, S_ACCFREE = S_ACC + 2, S_DONE = S_ACCFREE + 2, S_COUNT
 };
-constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + 2 * kBBytes + 256;
+constexpr uint32_t kSmem = 1024 + oBar + 512;
 
 struct Cut {
   int steps;        // per tile
   int tiles_k;      // output tiles along k
   long long units;  // tiles * steps
-  int ctas;
-  __host__ __device__ long long begin(int c) const { return units * c / ctas; }
+  int pairs;
+  __host__ __device__ long long begin(int c) const { return units * c / pairs; }
 };
 
 Cut cut_of(int rows, int n, int k) {
@@ -49,7 +64,7 @@ Cut cut_of(int rows, int n, int k) {
   c.steps = rows / kStep + (rows % kStep != 0);
   c.tiles_k = k / kTk + (k % kTk != 0);
   c.units = (long long)c.steps * c.tiles_k * (n / kTn + (n % kTn != 0));
-  c.ctas = (int)std::max<long long>(1, std::min<long long>(kCtas, c.units / kMinSteps));
+  c.pairs = (int)std::max<long long>(1, std::min<long long>(kPairs, c.units / kMinSteps));
   return c;
 }
 
@@ -91,226 +106,313 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t sbase = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t *smem = raw + (sbase - smem_u32(raw));
-  constexpr uint32_t oB = kStages * kStageBytes;
-  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + oB + 2 * kBBytes);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + oBar);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + S_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar + S_FULL + s, 1);
-      mbar_init(bar + S_EMPTY + s, 9);  // the MMAs and the eight converting warps
+      mbar_init(bar + S_DY + s, 1);
+      mbar_init(bar + S_CODES + s, 2);  // the loads and the scales
+      mbar_init(bar + S_EMPTY + s, 5);  // the MMAs and the converting warps
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(bar + S_BFULL + b, 8);
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(bar + S_BFULL + b, 8);  // converting warps of both CTAs
       mbar_init(bar + S_BEMPTY + b, 1);
     }
-    mbar_init(bar + S_ACC, 1);
-    mbar_init(bar + S_ACCFREE, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar + S_ACC + b, 1);
+      mbar_init(bar + S_ACCFREE + b, 16);  // adding warps of both CTAs
+    }
+    mbar_init(bar + S_DONE, 1);
     *abort_flag = 0;
     fence_barrier_init();
     if (TMA_DY) prefetch_tmap(&mdy);
     prefetch_tmap(&mx);
   }
-  if (warp == 2) tmem_alloc(tslot, 256);
+  if (warp == 2) tmem_alloc_pair(tslot, 512);
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tbase = *tslot;
-  const long long u0 = cut.begin(blockIdx.x), u1 = cut.begin(blockIdx.x + 1);
+  const long long u0 = cut.begin(pair), u1 = cut.begin(pair + 1);
+  const int total = (int)(u1 - u0);
   bool ok = true;
   auto wait = [&](int b, uint32_t par) {
     if (ok) ok = mbar_wait(bar + b, par, status, abort_flag);
     return ok;
   };
+  auto wait_warp = [&](int b, uint32_t par) {  // called by a whole warp, whose lanes agree on the result
+    wait(b, par);
+    return ok = __all_sync(0xffffffffu, ok);
+  };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + b);
   };
+  auto arrive_leader = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_pair(map_peer(smem_u32(bar + b), 0));
+  };
+  // Steps in order: a step's first n (this CTA's 128) and k (its block) of the
+  // tile, and first row.  Counted on, since two 64-bit divisions for each step
+  // take the loading thread longer than the MMAs of the step.
+  struct Place {
+    int n0, blk, r0, steps, tiles_k;
+    __device__ void advance() {
+      r0 += kStep;
+      if (r0 < steps * kStep) return;
+      r0 = 0;
+      blk += 2;
+      if (blk < 2 * tiles_k) return;
+      blk -= 2 * tiles_k;
+      n0 += kTn;
+    }
+  };
+  auto start = [&] {
+    const long long t = u0 / cut.steps;
+    return Place{(int)(t / cut.tiles_k) * kTn + rank * kBlock, (int)(t % cut.tiles_k) * 2 + rank,
+                 (int)(u0 - t * cut.steps) * kStep, cut.steps, cut.tiles_k};
+  };
 
-  if (warp == 0 && lane == 0) {
-    const int total = (int)(u1 - u0);
-    int i = 0;
-    for (; i < total; ++i) {
-      const int s = i % kStages;
-      if (i >= kStages && !wait(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1)) break;
-      const long long u = u0 + i, t = u / cut.steps;
-      const int r0 = (int)(u - t * cut.steps) * kStep, n0 = (int)(t / cut.tiles_k) * kTn,
-                kk = (int)(t % cut.tiles_k) * kTk;
-      const uint32_t at = sbase + s * kStageBytes;
-      mbar_arrive_expect_tx(bar + S_FULL + s, (TMA_DY ? kABytes : 0) + kCBytes);
-      if (TMA_DY) {
-        tma_load_2d(at, &mdy, bar + S_FULL + s, n0, r0);
-        tma_load_2d(at + kABytes / 2, &mdy, bar + S_FULL + s, n0 + 64, r0);
+  // Registers of the launch: 512 x 128.  The warpgroups' shares (56 + 96 + 2 x
+  // 176, times 128) come to 64512 of these 65536.
+  if (warp < 4) {
+    regs_dec<56>();
+    if (warp == 0 && lane == 0) {
+      Place p = start();
+      int i = 0;
+      for (; i < total; ++i, p.advance()) {
+        const int s = i % kStages;
+        if (i >= kStages && !wait(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1)) break;
+        const uint32_t at = sbase + s * kStageBytes;
+        if (TMA_DY) {
+          if (rank == 0) mbar_arrive_expect_tx(bar + S_DY + s, 2 * kDBytes);
+          const uint32_t full = map_peer(smem_u32(bar + S_DY + s), 0);
+          tma_load_2d_pair(at, &mdy, full, p.n0, p.r0);
+          tma_load_2d_pair(at + kDBytes / 2, &mdy, full, p.n0 + 64, p.r0);
+        }
+        mbar_arrive_expect_tx(bar + S_CODES + s, kCBytes);
+        tma_load_2d(at + kDBytes, &mx, bar + S_CODES + s, p.blk * kBlock, p.r0);
       }
-      tma_load_2d(at + kABytes, &mx, bar + S_FULL + s, kk, r0);
-      tma_load_2d(at + kABytes + kCBytes / 2, &mx, bar + S_FULL + s, kk + kBlock, r0);
-    }
-    for (int j = max(0, i - kStages); j < i; ++j) mbar_drain(bar + S_FULL + j % kStages, (uint32_t)(j / kStages) & 1);
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t id = make_idesc(kTn, kTk, true, true);
-    int i = 0, seg = 0;
-    for (long long u = u0; u < u1 && ok; ++seg) {
-      const long long end = min(u1, (u / cut.steps + 1) * cut.steps);
-      if (seg > 0 && !wait(S_ACCFREE, (seg - 1) & 1)) break;
-      tc_fence_after();
-      for (long long first = u; u < end; ++u, ++i) {
-        const int s = i % kStages, b = i & 1;
-        if (!wait(S_FULL + s, (uint32_t)(i / kStages) & 1) || !wait(S_BFULL + b, (uint32_t)(i >> 1) & 1)) break;
+      for (int j = max(0, i - kStages); j < i; ++j) {
+        mbar_drain(bar + S_CODES + j % kStages, (uint32_t)(j / kStages) & 1);
+        if (TMA_DY && rank == 0) mbar_drain(bar + S_DY + j % kStages, (uint32_t)(j / kStages) & 1);
+      }
+    } else if (warp == 1 && rank == 0) {
+      const bool issues = elect_lane();
+      const uint32_t id = make_idesc(kTn, kTk, true, true);
+      int i = 0, win = 0;
+      for (long long u = u0; u < u1 && ok; ++win) {
+        const long long end = min(min(u1, (u / cut.steps + 1) * cut.steps), u + kWindow);
+        if (win >= 2 && !wait_warp(S_ACCFREE + (win & 1), (uint32_t)((win >> 1) - 1) & 1)) break;
         tc_fence_after();
-        const uint64_t da = desc_mnmajor(sbase + s * kStageBytes, kStep, 0, 0);
-        const uint64_t db = desc_mnmajor(sbase + oB + b * kBBytes, kStep, 0, 0);
+        const uint32_t acc = tbase + (win & 1) * kTk;
+        for (long long first = u; u < end; ++u, ++i) {
+          const int s = i % kStages, b = i % kBufs;
+          if (TMA_DY && !wait_warp(S_DY + s, (uint32_t)(i / kStages) & 1)) break;
+          if (!wait_warp(S_BFULL + b, (uint32_t)(i / kBufs) & 1)) break;
+          tc_fence_after();
+          const uint64_t da = desc_mnmajor(sbase + s * kStageBytes, kStep, 0, 0);
+          const uint64_t db = desc_mnmajor(sbase + oB + b * kBBytes, kStep, 0, 0);
 #pragma unroll
-        for (int j = 0; j < kStep / 16; ++j)
-          mma_bf16(tbase, da + (uint64_t)(j * 128), db + (uint64_t)(j * 128), id, u > first || j > 0);
-        mma_commit(bar + S_EMPTY + s);
-        mma_commit(bar + S_BEMPTY + b);
+          for (int j = 0; j < kStep / 16; ++j)
+            if (issues) mma_bf16_pair(acc, da + (uint64_t)(j * 128), db + (uint64_t)(j * 128), id, u > first || j > 0);
+          if (issues) {
+            mma_commit_pair(bar + S_EMPTY + s);
+            mma_commit_pair(bar + S_BEMPTY + b);
+          }
+          __syncwarp();
+        }
+        if (ok && issues) mma_commit_pair(bar + S_ACC + (win & 1));
+        __syncwarp();
       }
-      if (ok) mma_commit(bar + S_ACC);
+      if (issues) mma_commit_pair(bar + S_DONE);
+      __syncwarp();
+      mbar_drain(bar + S_DONE, 0);
+    } else if (warp == 3) {
+      // Factors of each step's rows, two rows a lane.  Four steps' scale bytes
+      // are on their way from memory while one step's are stored.
+      constexpr int kAhead = 4;
+      int byte[kAhead][2];
+      Place p = start();
+      auto fetch = [&](int i, int (&v)[2]) {  // steps in order
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = p.r0 + lane + 32 * h;
+          v[h] = i < total && r < rows && p.blk * kBlock < k ? (int)__ldg(scales + (size_t)r * pitch + p.blk) : 127;
+        }
+        p.advance();
+      };
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) fetch(a, byte[a]);
+      for (int i0 = 0; i0 < total && ok; i0 += kAhead) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int i = i0 + a, s = i % kStages;
+          if (i < total && ok && (i < kStages || wait_warp(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1))) {
+            uint2 *table = reinterpret_cast<uint2 *>(smem + oTable + s * kTable);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint2 f;
+              f.x = factor(byte[a][h], f.y);
+              table[lane + 32 * h] = f;
+            }
+            arrive(S_CODES + s);
+            fetch(i + kAhead, byte[a]);
+          }
+        }
+      }
     }
-  } else if (warp >= 4) {
-    // thread: 16 codes of rows r0 + 16 j, always of the same 128-column block
-    const int ct = tid - 128, chunk = ct & 15, row0 = ct >> 4, half = chunk >> 3;
+  } else if (warp < 8) {
+    regs_dec<96>();
+    // thread: 16 codes of rows row0 + 16 j
+    const int ct = tid - 128, chunk = ct & 7, row0 = ct >> 3;
+    Place p = start();
+    for (int i = 0; i < total && ok; ++i, p.advance()) {
+      const int s = i % kStages, b = i % kBufs;
+      if (!wait(S_CODES + s, (uint32_t)(i / kStages) & 1)) break;
+      uint4 code[4];
+      uint2 f[4];
+      const uint32_t from = sbase + s * kStageBytes + kDBytes + chunk * 16;
+      const uint2 *table = reinterpret_cast<const uint2 *>(smem + oTable + s * kTable);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ld_shared_v4(from + (row0 + 16 * j) * kBlock, code[j].x, code[j].y, code[j].z, code[j].w);
+        f[j] = table[row0 + 16 * j];
+      }
+      if (!TMA_DY) {  // rows that TMA cannot step over: these warps load them into the same layout
+        for (int x = ct; x < kStep * kBlock; x += 128) {
+          const int r = x / kBlock, c = x % kBlock;
+          const __nv_bfloat16 v =
+              p.r0 + r < rows && p.n0 + c < n ? dy[(size_t)(p.r0 + r) * n + p.n0 + c] : __float2bfloat16_rn(0.f);
+          *reinterpret_cast<__nv_bfloat16 *>(smem + s * kStageBytes + sw128_offset(r, c, kStep)) = v;
+        }
+      }
+      if (i >= kBufs && !wait(S_BEMPTY + b, (uint32_t)(i / kBufs - 1) & 1)) break;
+      const uint32_t to = sbase + oB + b * kBBytes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = mul_bf16x2(widen(w[e], 0x1404), f[j].x);
+          o[2 * e + 1] = mul_bf16x2(widen(w[e], 0x3424), f[j].x);
+        }
+        if (f[j].y) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f[j].y);
+        }
+        // the two 16-byte halves in an order that keeps eight lanes on distinct banks
+        const int r = row0 + 16 * j;
+        const uint32_t a0 = to + sw128_offset(r, 16 * chunk, kStep), a1 = to + sw128_offset(r, 16 * chunk + 8, kStep);
+        if (chunk & 4) {
+          st_shared_v4(a1, o[4], o[5], o[6], o[7]);
+          st_shared_v4(a0, o[0], o[1], o[2], o[3]);
+        } else {
+          st_shared_v4(a0, o[0], o[1], o[2], o[3]);
+          st_shared_v4(a1, o[4], o[5], o[6], o[7]);
+        }
+      }
+      fence_async_smem();
+      arrive_leader(S_BFULL + b);
+      arrive(S_EMPTY + s);
+    }
+  } else {
+    regs_inc<176>();
+    // this thread's row of the tile (a TMEM lane), 128 of its 256 columns
     const uint32_t lanes = 32u * (warp & 3);
-    int i = 0, seg = 0;
-    for (long long u = u0; u < u1 && ok; ++seg) {
+    const int c0 = warp < 12 ? 0 : 128, nr = rank * kBlock + (int)lanes + lane;
+    int win = 0;
+    for (long long u = u0; u < u1 && ok;) {
       const long long t = u / cut.steps, end = min(u1, (t + 1) * cut.steps);
       const bool whole = u == t * cut.steps && end == (t + 1) * cut.steps, first_seg = u == u0;
-      const int n0 = (int)(t / cut.tiles_k) * kTn, kk = (int)(t % cut.tiles_k) * kTk;
-      const int blk = kk / kBlock + half;
-      const bool has = blk * kBlock < k;
-      auto scale_at = [&](long long step, int j) {
-        const long long r = step * kStep + row0 + 16 * j;
-        return has && r < rows ? (int)__ldg(scales + (size_t)r * pitch + blk) : 127;
-      };
-      int byte[4];
+      float sum[128];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) byte[j] = scale_at(u - t * cut.steps, j);
-      for (; u < end; ++u, ++i) {
-        const int s = i % kStages, b = i & 1;
-        if (!wait(S_FULL + s, (uint32_t)(i / kStages) & 1)) break;
-        uint4 code[4];
-        const uint32_t from = sbase + s * kStageBytes + kABytes + half * (kCBytes / 2) + (chunk & 7) * 16;
+      for (int e = 0; e < 128; ++e) sum[e] = 0.f;
+      for (; u < end && ok; u = min(end, u + kWindow), ++win) {
+        wait_warp(S_ACC + (win & 1), (uint32_t)(win >> 1) & 1);
+        tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ld_shared_v4(from + (row0 + 16 * j) * kBlock, code[j].x, code[j].y, code[j].z, code[j].w);
-        int next[4];
-        const long long step = u - t * cut.steps;
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          tmem_ld32(tmem_addr(tbase, lanes, (win & 1) * kTk + c0 + c), v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) next[j] = u + 1 < end ? scale_at(step + 1, j) : 127;
-        if (!TMA_DY) {  // rows that TMA cannot step over: this warp group's own loads into the same layout
-          for (int x = ct; x < kStep * kTn; x += 256) {
-            const int r = x / kTn, c = x % kTn;
-            const long long gr = step * kStep + r;
-            const __nv_bfloat16 v = gr < rows && n0 + c < n ? dy[(size_t)gr * n + n0 + c] : __float2bfloat16_rn(0.f);
-            *reinterpret_cast<__nv_bfloat16 *>(smem + s * kStageBytes + sw128_offset(r, c, kStep)) = v;
-          }
+          for (int e = 0; e < 32; ++e) sum[c + e] += v[e];
         }
-        if (i >= 2 && !wait(S_BEMPTY + b, (uint32_t)((i >> 1) - 1) & 1)) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t second;
-          const uint32_t f = factor(byte[j], second);
-          const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[2 * e] = mul_bf16x2(widen(w[e], 0x1404), f);
-            o[2 * e + 1] = mul_bf16x2(widen(w[e], 0x3424), f);
-          }
-          if (second) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], second);
-          }
-          const int r = row0 + 16 * j;
-          const uint32_t to = sbase + oB + b * kBBytes;
-          // the two 16-byte halves in an order that keeps a warp's stores on distinct banks
-          const uint32_t a0 = to + sw128_offset(r, 16 * chunk, kStep), a1 = to + sw128_offset(r, 16 * chunk + 8, kStep);
-          if (chunk & 4) {
-            st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-            st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-          } else {
-            st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-            st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-          }
-          byte[j] = next[j];
-        }
-        fence_async_smem();
-        arrive(S_BFULL + b);
-        arrive(S_EMPTY + s);
+        tc_fence_before();
+        arrive_leader(S_ACCFREE + (win & 1));
       }
-      if (!wait(S_ACC, seg & 1)) break;
-      tc_fence_after();
-      // this thread's row of the tile, 128 of its 256 columns: into dw, or into this CTA's partial tile
-      const int nr = (int)lanes + lane, c0 = warp < 8 ? 0 : 128;
+      if (!ok) break;
+      // into dw, or into this pair's partial tile
+      const int n0 = (int)(t / cut.tiles_k) * kTn, kk = (int)(t % cut.tiles_k) * kTk + c0;
       float *to = whole ? dw + (size_t)(n0 + nr) * k + kk
-                        : partial + ((size_t)blockIdx.x * 2 + (first_seg ? 0 : 1)) * (kTn * kTk) + (size_t)nr * kTk;
+                        : partial + ((size_t)pair * 2 + (first_seg ? 0 : 1)) * (kTn * kTk) + (size_t)nr * kTk + c0;
       const int left = whole ? (n0 + nr < n ? k - kk : 0) : kTk;
-      const bool vec = !whole || wide, add = whole && accumulate;
-      for (int c = c0; c < c0 + 128; c += 32) {
-        float v[32];
-        __syncwarp();
-        tmem_ld32(tmem_addr(tbase, lanes, c), v);
-        if (vec) {
+      const bool add = whole && accumulate;
+      if (!whole || wide) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            if (c + e < left) {
-              float4 *p = reinterpret_cast<float4 *>(to + c + e);
-              float4 x = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-              if (add) {
-                const float4 o = *p;
-                x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
-              }
-              *p = x;
+        for (int e = 0; e < 128; e += 4) {
+          if (e < left) {
+            float4 *p = reinterpret_cast<float4 *>(to + e);
+            float4 x = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+            if (add) {
+              const float4 o = *p;
+              x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
             }
+            *p = x;
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c + e < left) to[c + e] = add ? to[c + e] + v[e] : v[e];
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e < left) to[e] = add ? to[e] + sum[e] : sum[e];
       }
-      tc_fence_before();
-      arrive(S_ACCFREE);
     }
   }
-  __syncthreads();
-  if (warp == 2) tmem_dealloc(tbase, 256);
+  __syncwarp();
+  cluster_sync();
+  if (warp == 2) tmem_dealloc_pair(tbase, 512);
 }
 
-// dw of the tiles that several CTAs share: one CTA for 32 rows of such a tile.
+// dw of the tiles that several pairs share, four columns a thread.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const float *partial, float *dw, Cut cut, int accumulate, int n,
                                                          int k) {
   const long long t = blockIdx.x, first = t * cut.steps, last = first + cut.steps - 1;
-  // the CTA that holds unit u: the largest c with begin(c) <= u
+  // the pair that holds unit u: the largest c with begin(c) <= u
   auto owner = [&](long long u) {
-    int c = (int)(u * cut.ctas / cut.units);
+    int c = (int)(u * cut.pairs / cut.units);
     while (cut.begin(c + 1) <= u) ++c;
     while (cut.begin(c) > u) --c;
     return c;
   };
-  const int ca = owner(first), cb = owner(last);
-  if (ca == cb) return;  // held by one CTA, written in full
-  const int n0 = (int)(t / cut.tiles_k) * kTn, kk = (int)(t % cut.tiles_k) * kTk;
-  for (int x = threadIdx.x; x < 32 * kTk; x += 256) {
-    const int r = blockIdx.y * 32 + x / kTk, c = x % kTk;
-    if (n0 + r >= n || kk + c >= k) continue;
-    float v = 0.f;
-    for (int i = ca; i <= cb; ++i) {
-      // a CTA's first segment lies in slot 0; a later one, which begins its tile, in slot 1
-      const int slot = cut.begin(i) / cut.steps == t ? 0 : 1;
-      v += partial[((size_t)i * 2 + slot) * (kTn * kTk) + (size_t)r * kTk + c];
-    }
-    float *to = dw + (size_t)(n0 + r) * k + kk + c;
-    *to = accumulate ? *to + v : v;
+  const int pa = owner(first), pb = owner(last);
+  if (pa == pb) return;  // held by one pair, written in full
+  const int at = (int)blockIdx.y * 1024 + threadIdx.x * 4, r = at / kTk, c = at % kTk;
+  const int nn = (int)(t / cut.tiles_k) * kTn + r, kk = (int)(t % cut.tiles_k) * kTk + c;
+  if (nn >= n || kk >= k) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  // a pair's first segment lies in slot 0; a later one, which begins its tile, in slot 1
+  const int slot = cut.begin(pa) / cut.steps == t ? 0 : 1;
+#pragma unroll 4
+  for (int i = pa; i <= pb; ++i) {
+    const float4 x = *reinterpret_cast<const float4 *>(partial + ((size_t)i * 2 + (i == pa ? slot : 0)) * (kTn * kTk) + at);
+    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
   }
+  const float s[4] = {v.x, v.y, v.z, v.w};
+  float *to = dw + (size_t)nn * k + kk;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (kk + e < k) to[e] = accumulate ? to[e] + s[e] : s[e];
 }
 
 }  // namespace
 
 size_t wgrad_workspace(int rows, int n, int k) {
   if (rows == 0 || n == 0 || k == 0) return 0;
-  return (size_t)cut_of(rows, n, k).ctas * 2 * kTn * kTk * sizeof(float);
+  return (size_t)cut_of(rows, n, k).pairs * 2 * kTn * kTk * sizeof(float);
 }
 
 cudaError_t wgrad(const void *dy, const void *x_codes, const void *x_scales, float *dw, bool accumulate,
@@ -327,18 +429,29 @@ cudaError_t wgrad(const void *dy, const void *x_codes, const void *x_scales, flo
   auto kern = tma ? wgrad_kernel<true> : wgrad_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * cut.pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   {
     ProfScope ps("q8_wgrad", st);
-    kern<<<cut.ctas, kThreads, kSmem, st>>>(mdy, mx, static_cast<const __nv_bfloat16 *>(dy),
-                                            static_cast<const uint8_t *>(x_scales), dw,
-                                            static_cast<float *>(workspace), cut, accumulate ? 1 : 0, rows, n, k,
-                                            scale_pitch(k),
-                                            k % 4 == 0 && (reinterpret_cast<uintptr_t>(dw) & 15) == 0, status);
-    e = cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, kern, mdy, mx, static_cast<const __nv_bfloat16 *>(dy),
+                           static_cast<const uint8_t *>(x_scales), dw, static_cast<float *>(workspace), cut,
+                           accumulate ? 1 : 0, rows, n, k, scale_pitch(k),
+                           k % 4 == 0 && (reinterpret_cast<uintptr_t>(dw) & 15) == 0 ? 1 : 0, status);
+    if (e == cudaSuccess) e = cudaGetLastError();
   }
-  if (e != cudaSuccess || cut.ctas == 1) return e;
+  if (e != cudaSuccess || cut.pairs == 1) return e;
   ProfScope ps("q8_wgrad_join", st);
-  wgrad_join_kernel<<<dim3((unsigned)(cut.units / cut.steps), kTn / 32), 256, 0, st>>>(
+  wgrad_join_kernel<<<dim3((unsigned)(cut.units / cut.steps), kTn * kTk / 1024), 256, 0, st>>>(
       static_cast<const float *>(workspace), dw, cut, accumulate ? 1 : 0, n, k);
   return cudaGetLastError();
 }
