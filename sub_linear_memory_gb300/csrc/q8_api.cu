@@ -299,7 +299,8 @@ slim_status slim_q8_wgrad(const void *dy, const void *x_codes, const void *x_sca
   }
   SLIM_TRY(check_rows<bf16>(dy));
   SLIM_TRY(check_mat(x_codes, x_scales, false));
-  if (!workspace || workspace_bytes < wgrad_workspace(rows, n, k)) return SLIM_ERR_WORKSPACE;
+  const size_t need = wgrad_workspace(rows, n, k);
+  if (need && (!workspace || workspace_bytes < need)) return SLIM_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return SLIM_ERR_UNSUPPORTED;
   int *status = slim::device_status_ptr();
   if (!status) return SLIM_ERR_CUDA;

@@ -19,11 +19,15 @@
 // registers of eight other warps, which add with rounding to nearest, while
 // the MMAs go on in a second accumulator.
 //
-// Split: the rows are cut into steps of 64, and all steps of all tiles form
-// one line that is cut evenly over the pairs, so every SM has the same share
-// whatever the shape; a pair that does not hold all steps of a tile leaves a
-// partial tile in the workspace, and a second kernel adds the partials in the
-// order of the line.
+// Split: the rows are cut into steps of 64.  While there are as many tiles as
+// pairs, a pair takes a whole tile.  The remaining tiles, fewer than the pairs,
+// are cut along the rows: each into equal parts, one for a pair, and what the
+// left-over pairs can take from the end of every tile.  All pairs then have
+// the same number of steps, and those on different tiles pass over the same
+// rows at the same time: dy and x come from DRAM once (one even cut of the
+// line of all steps put them at different rows, and 65536 x 1024 x 4096 read
+// 3.2 GB, 612 us).  Parts of a tile go to the workspace as partial tiles, which a
+// second kernel adds in a fixed order.
 #include <algorithm>
 
 #include "kernels.h"
@@ -51,22 +55,85 @@ enum {
 };
 constexpr uint32_t kSmem = 1024 + oBar + 512;
 
+// One pair's part of a tile: steps [s0, s1), and the workspace slot of its
+// partial tile (-1: the whole tile, straight into dw).
+struct Seg {
+  int tile, s0, s1, slot;
+};
+
 struct Cut {
-  int steps;        // per tile
-  int tiles_k;      // output tiles along k
-  long long units;  // tiles * steps
-  int pairs;
-  __host__ __device__ long long begin(int c) const { return units * c / pairs; }
+  int steps;          // of a tile
+  int tiles_k;        // tiles along k
+  int pairs, waves;   // tiles [0, waves * pairs) are taken whole
+  int rest;           // tiles after those, each cut into `parts` of `part` steps
+  int parts, part;
+  int tail, extras;   // and `tail` last steps, shared out over the `extras` left-over pairs
+
+  __host__ __device__ long long tail_begin(int e) const { return (long long)rest * tail * e / extras; }
+  // Segment `i` of a pair; false past its last.
+  __host__ __device__ bool get(int pair, int i, Seg &s) const {
+    if (i < waves) {
+      s = Seg{i * pairs + pair, 0, steps, -1};
+      return true;
+    }
+    i -= waves;
+    if (pair < parts * rest) {
+      const int t = pair % rest, j = pair / rest, s0 = j * part, s1 = s0 + part < steps ? s0 + part : steps;
+      s = Seg{waves * pairs + t, s0, s1, t * parts + j};
+      return i == 0 && s0 < s1;
+    }
+    if (tail == 0) return false;
+    const int e = pair - parts * rest;
+    const long long lo = tail_begin(e), hi = tail_begin(e + 1), t = lo / tail + i, t0 = t * tail;
+    const long long a = lo > t0 ? lo : t0, b = hi < t0 + tail ? hi : t0 + tail;
+    s = Seg{waves * pairs + (int)t, parts * part + (int)(a - t0), parts * part + (int)(b - t0),
+            parts * rest + (int)t + e};
+    return a < b;
+  }
 };
 
 Cut cut_of(int rows, int n, int k) {
   Cut c;
   c.steps = rows / kStep + (rows % kStep != 0);
   c.tiles_k = k / kTk + (k % kTk != 0);
-  c.units = (long long)c.steps * c.tiles_k * (n / kTn + (n % kTn != 0));
-  c.pairs = (int)std::max<long long>(1, std::min<long long>(kPairs, c.units / kMinSteps));
+  const long long tiles = (long long)c.tiles_k * (n / kTn + (n % kTn != 0));
+  c.pairs = (int)std::min<long long>(kPairs, std::max(tiles, tiles * c.steps / kMinSteps));
+  c.waves = (int)(tiles / c.pairs);
+  c.rest = (int)(tiles % c.pairs);
+  c.parts = c.part = c.tail = c.extras = 0;
+  if (c.rest) {
+    c.parts = c.pairs / c.rest;
+    c.part = (int)(((long long)c.steps * c.rest + c.pairs - 1) / c.pairs);
+    c.extras = c.pairs - c.parts * c.rest;
+    c.tail = c.extras ? std::max(0, c.steps - c.parts * c.part) : 0;
+  }
   return c;
 }
+
+// Partial tiles: one for each part, and of the tail one more than there are
+// cuts between its tiles and between the pairs that share it.
+int slots_of(const Cut &c) { return c.rest ? c.parts * c.rest + (c.tail ? c.rest + c.extras : 0) : 0; }
+
+// A pair's steps in order.
+struct Walk {
+  const Cut &cut;
+  int pair, rank, i = 0;
+  Seg seg{0, 0, 0, -1};
+  bool more;
+  int step = 0, n0 = 0, blk = 0;  // this CTA's first n and block of k in the tile
+  __device__ Walk(const Cut &c, int p, int r) : cut(c), pair(p), rank(r) { enter(); }
+  __device__ void enter() {
+    more = cut.get(pair, i, seg);
+    step = seg.s0;
+    n0 = seg.tile / cut.tiles_k * kTn + rank * kBlock;
+    blk = seg.tile % cut.tiles_k * 2 + rank;
+  }
+  __device__ void next() {
+    if (++step < seg.s1) return;
+    ++i;
+    enter();
+  }
+};
 
 // Two e4m3 codes in bytes 0 and 1 (or 2 and 3) of w as bf16 bits: sign and the
 // seven bits moved to the top of exponent and fraction, i.e. the value times
@@ -136,8 +203,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tbase = *tslot;
-  const long long u0 = cut.begin(pair), u1 = cut.begin(pair + 1);
-  const int total = (int)(u1 - u0);
   bool ok = true;
   auto wait = [&](int b, uint32_t par) {
     if (ok) ok = mbar_wait(bar + b, par, status, abort_flag);
@@ -155,46 +220,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive_pair(map_peer(smem_u32(bar + b), 0));
   };
-  // Steps in order: a step's first n (this CTA's 128) and k (its block) of the
-  // tile, and first row.  Counted on, since two 64-bit divisions for each step
-  // take the loading thread longer than the MMAs of the step.
-  struct Place {
-    int n0, blk, r0, steps, tiles_k;
-    __device__ void advance() {
-      r0 += kStep;
-      if (r0 < steps * kStep) return;
-      r0 = 0;
-      blk += 2;
-      if (blk < 2 * tiles_k) return;
-      blk -= 2 * tiles_k;
-      n0 += kTn;
-    }
-  };
-  auto start = [&] {
-    const long long t = u0 / cut.steps;
-    return Place{(int)(t / cut.tiles_k) * kTn + rank * kBlock, (int)(t % cut.tiles_k) * 2 + rank,
-                 (int)(u0 - t * cut.steps) * kStep, cut.steps, cut.tiles_k};
-  };
-
   // Registers of the launch: 512 x 128.  The warpgroups' shares (56 + 96 + 2 x
   // 176, times 128) come to 64512 of these 65536.
   if (warp < 4) {
     regs_dec<56>();
     if (warp == 0 && lane == 0) {
-      Place p = start();
       int i = 0;
-      for (; i < total; ++i, p.advance()) {
+      for (Walk p(cut, pair, rank); p.more; p.next(), ++i) {
+        const int r0 = p.step * kStep;
         const int s = i % kStages;
         if (i >= kStages && !wait(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1)) break;
         const uint32_t at = sbase + s * kStageBytes;
         if (TMA_DY) {
           if (rank == 0) mbar_arrive_expect_tx(bar + S_DY + s, 2 * kDBytes);
           const uint32_t full = map_peer(smem_u32(bar + S_DY + s), 0);
-          tma_load_2d_pair(at, &mdy, full, p.n0, p.r0);
-          tma_load_2d_pair(at + kDBytes / 2, &mdy, full, p.n0 + 64, p.r0);
+          tma_load_2d_pair(at, &mdy, full, p.n0, r0);
+          tma_load_2d_pair(at + kDBytes / 2, &mdy, full, p.n0 + 64, r0);
         }
         mbar_arrive_expect_tx(bar + S_CODES + s, kCBytes);
-        tma_load_2d(at + kDBytes, &mx, bar + S_CODES + s, p.blk * kBlock, p.r0);
+        tma_load_2d(at + kDBytes, &mx, bar + S_CODES + s, p.blk * kBlock, r0);
       }
       for (int j = max(0, i - kStages); j < i; ++j) {
         mbar_drain(bar + S_CODES + j % kStages, (uint32_t)(j / kStages) & 1);
@@ -204,29 +248,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool issues = elect_lane();
       const uint32_t id = make_idesc(kTn, kTk, true, true);
       int i = 0, win = 0;
-      for (long long u = u0; u < u1 && ok; ++win) {
-        const long long end = min(min(u1, (u / cut.steps + 1) * cut.steps), u + kWindow);
-        if (win >= 2 && !wait_warp(S_ACCFREE + (win & 1), (uint32_t)((win >> 1) - 1) & 1)) break;
-        tc_fence_after();
-        const uint32_t acc = tbase + (win & 1) * kTk;
-        for (long long first = u; u < end; ++u, ++i) {
-          const int s = i % kStages, b = i % kBufs;
-          if (TMA_DY && !wait_warp(S_DY + s, (uint32_t)(i / kStages) & 1)) break;
-          if (!wait_warp(S_BFULL + b, (uint32_t)(i / kBufs) & 1)) break;
+      Seg seg;
+      for (int x = 0; ok && cut.get(pair, x, seg); ++x) {
+        for (int first = seg.s0; first < seg.s1 && ok; first += kWindow, ++win) {
+          if (win >= 2 && !wait_warp(S_ACCFREE + (win & 1), (uint32_t)((win >> 1) - 1) & 1)) break;
           tc_fence_after();
-          const uint64_t da = desc_mnmajor(sbase + s * kStageBytes, kStep, 0, 0);
-          const uint64_t db = desc_mnmajor(sbase + oB + b * kBBytes, kStep, 0, 0);
+          const uint32_t acc = tbase + (win & 1) * kTk;
+          const int end = min(first + kWindow, seg.s1);
+          for (int step = first; step < end; ++step, ++i) {
+            const int s = i % kStages, b = i % kBufs;
+            if (TMA_DY && !wait_warp(S_DY + s, (uint32_t)(i / kStages) & 1)) break;
+            if (!wait_warp(S_BFULL + b, (uint32_t)(i / kBufs) & 1)) break;
+            tc_fence_after();
+            const uint64_t da = desc_mnmajor(sbase + s * kStageBytes, kStep, 0, 0);
+            const uint64_t db = desc_mnmajor(sbase + oB + b * kBBytes, kStep, 0, 0);
 #pragma unroll
-          for (int j = 0; j < kStep / 16; ++j)
-            if (issues) mma_bf16_pair(acc, da + (uint64_t)(j * 128), db + (uint64_t)(j * 128), id, u > first || j > 0);
-          if (issues) {
-            mma_commit_pair(bar + S_EMPTY + s);
-            mma_commit_pair(bar + S_BEMPTY + b);
+            for (int j = 0; j < kStep / 16; ++j)
+              if (issues)
+                mma_bf16_pair(acc, da + (uint64_t)(j * 128), db + (uint64_t)(j * 128), id, step > first || j > 0);
+            if (issues) {
+              mma_commit_pair(bar + S_EMPTY + s);
+              mma_commit_pair(bar + S_BEMPTY + b);
+            }
+            __syncwarp();
           }
+          if (ok && issues) mma_commit_pair(bar + S_ACC + (win & 1));
           __syncwarp();
         }
-        if (ok && issues) mma_commit_pair(bar + S_ACC + (win & 1));
-        __syncwarp();
       }
       if (issues) mma_commit_pair(bar + S_DONE);
       __syncwarp();
@@ -236,22 +284,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // are on their way from memory while one step's are stored.
       constexpr int kAhead = 4;
       int byte[kAhead][2];
-      Place p = start();
-      auto fetch = [&](int i, int (&v)[2]) {  // steps in order
+      Walk p(cut, pair, rank);
+      auto fetch = [&](int (&v)[2]) {  // steps in order; -1 past the last
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = p.r0 + lane + 32 * h;
-          v[h] = i < total && r < rows && p.blk * kBlock < k ? (int)__ldg(scales + (size_t)r * pitch + p.blk) : 127;
+          const int r = p.step * kStep + lane + 32 * h;
+          v[h] = !p.more                                ? -1
+                 : r < rows && p.blk * kBlock < k ? (int)__ldg(scales + (size_t)r * pitch + p.blk)
+                                                        : 127;
         }
-        p.advance();
+        if (p.more) p.next();
       };
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) fetch(a, byte[a]);
-      for (int i0 = 0; i0 < total && ok; i0 += kAhead) {
+      for (int a = 0; a < kAhead; ++a) fetch(byte[a]);
+      for (int i0 = 0; byte[0][0] >= 0 && ok; i0 += kAhead) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
           const int i = i0 + a, s = i % kStages;
-          if (i < total && ok && (i < kStages || wait_warp(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1))) {
+          if (byte[a][0] >= 0 && ok && (i < kStages || wait_warp(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1))) {
             uint2 *table = reinterpret_cast<uint2 *>(smem + oTable + s * kTable);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -260,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               table[lane + 32 * h] = f;
             }
             arrive(S_CODES + s);
-            fetch(i + kAhead, byte[a]);
+            fetch(byte[a]);
           }
         }
       }
@@ -269,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<96>();
     // thread: 16 codes of rows row0 + 16 j
     const int ct = tid - 128, chunk = ct & 7, row0 = ct >> 3;
-    Place p = start();
-    for (int i = 0; i < total && ok; ++i, p.advance()) {
+    int i = 0;
+    for (Walk p(cut, pair, rank); p.more && ok; p.next(), ++i) {
       const int s = i % kStages, b = i % kBufs;
       if (!wait(S_CODES + s, (uint32_t)(i / kStages) & 1)) break;
       uint4 code[4];
@@ -283,10 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         f[j] = table[row0 + 16 * j];
       }
       if (!TMA_DY) {  // rows that TMA cannot step over: these warps load them into the same layout
+        const int r0 = p.step * kStep;
         for (int x = ct; x < kStep * kBlock; x += 128) {
           const int r = x / kBlock, c = x % kBlock;
           const __nv_bfloat16 v =
-              p.r0 + r < rows && p.n0 + c < n ? dy[(size_t)(p.r0 + r) * n + p.n0 + c] : __float2bfloat16_rn(0.f);
+              r0 + r < rows && p.n0 + c < n ? dy[(size_t)(r0 + r) * n + p.n0 + c] : __float2bfloat16_rn(0.f);
           *reinterpret_cast<__nv_bfloat16 *>(smem + s * kStageBytes + sw128_offset(r, c, kStep)) = v;
         }
       }
@@ -326,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = 32u * (warp & 3);
     const int c0 = warp < 12 ? 0 : 128, nr = rank * kBlock + (int)lanes + lane;
     int win = 0;
-    for (long long u = u0; u < u1 && ok;) {
-      const long long t = u / cut.steps, end = min(u1, (t + 1) * cut.steps);
-      const bool whole = u == t * cut.steps && end == (t + 1) * cut.steps, first_seg = u == u0;
+    Seg seg;
+    for (int x = 0; ok && cut.get(pair, x, seg); ++x) {
+      const bool whole = seg.slot < 0;
       float sum[128];
 #pragma unroll
       for (int e = 0; e < 128; ++e) sum[e] = 0.f;
-      for (; u < end && ok; u = min(end, u + kWindow), ++win) {
+      for (int first = seg.s0; first < seg.s1 && ok; first += kWindow, ++win) {
         wait_warp(S_ACC + (win & 1), (uint32_t)(win >> 1) & 1);
         tc_fence_after();
 #pragma unroll
@@ -347,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // into dw, or into this pair's partial tile
-      const int n0 = (int)(t / cut.tiles_k) * kTn, kk = (int)(t % cut.tiles_k) * kTk + c0;
+      const int n0 = seg.tile / cut.tiles_k * kTn, kk = seg.tile % cut.tiles_k * kTk + c0;
       float *to = whole ? dw + (size_t)(n0 + nr) * k + kk
-                        : partial + ((size_t)pair * 2 + (first_seg ? 0 : 1)) * (kTn * kTk) + (size_t)nr * kTk + c0;
+                        : partial + (size_t)seg.slot * (kTn * kTk) + (size_t)nr * kTk + c0;
       const int left = whole ? (n0 + nr < n ? k - kk : 0) : kTk;
       const bool add = whole && accumulate;
       if (!whole || wide) {
@@ -377,29 +428,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc_pair(tbase, 512);
 }
 
-// dw of the tiles that several pairs share, four columns a thread.
+// dw of the tiles that are cut along the rows, four columns a thread.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const float *partial, float *dw, Cut cut, int accumulate, int n,
                                                          int k) {
-  const long long t = blockIdx.x, first = t * cut.steps, last = first + cut.steps - 1;
-  // the pair that holds unit u: the largest c with begin(c) <= u
-  auto owner = [&](long long u) {
-    int c = (int)(u * cut.pairs / cut.units);
-    while (cut.begin(c + 1) <= u) ++c;
-    while (cut.begin(c) > u) --c;
-    return c;
-  };
-  const int pa = owner(first), pb = owner(last);
-  if (pa == pb) return;  // held by one pair, written in full
+  const int t = blockIdx.x, tile = cut.waves * cut.pairs + t;
   const int at = (int)blockIdx.y * 1024 + threadIdx.x * 4, r = at / kTk, c = at % kTk;
-  const int nn = (int)(t / cut.tiles_k) * kTn + r, kk = (int)(t % cut.tiles_k) * kTk + c;
+  const int nn = tile / cut.tiles_k * kTn + r, kk = tile % cut.tiles_k * kTk + c;
   if (nn >= n || kk >= k) return;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  // a pair's first segment lies in slot 0; a later one, which begins its tile, in slot 1
-  const int slot = cut.begin(pa) / cut.steps == t ? 0 : 1;
-#pragma unroll 4
-  for (int i = pa; i <= pb; ++i) {
-    const float4 x = *reinterpret_cast<const float4 *>(partial + ((size_t)i * 2 + (i == pa ? slot : 0)) * (kTn * kTk) + at);
+  auto add = [&](int slot) {
+    const float4 x = *reinterpret_cast<const float4 *>(partial + (size_t)slot * (kTn * kTk) + at);
     v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+  };
+  const int parts = min(cut.parts, (cut.steps + cut.part - 1) / cut.part);
+#pragma unroll 4
+  for (int j = 0; j < parts; ++j) add(t * cut.parts + j);
+  if (cut.tail) {
+    // the left-over pairs that hold steps of this tile's tail
+    const long long first = (long long)t * cut.tail, last = first + cut.tail;
+    for (int e = 0; e < cut.extras; ++e)
+      if (max(cut.tail_begin(e), first) < min(cut.tail_begin(e + 1), last)) add(cut.parts * cut.rest + t + e);
   }
   const float s[4] = {v.x, v.y, v.z, v.w};
   float *to = dw + (size_t)nn * k + kk;
@@ -412,7 +460,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float *partial, f
 
 size_t wgrad_workspace(int rows, int n, int k) {
   if (rows == 0 || n == 0 || k == 0) return 0;
-  return (size_t)cut_of(rows, n, k).pairs * 2 * kTn * kTk * sizeof(float);
+  return (size_t)slots_of(cut_of(rows, n, k)) * kTn * kTk * sizeof(float);
 }
 
 cudaError_t wgrad(const void *dy, const void *x_codes, const void *x_scales, float *dw, bool accumulate,
@@ -449,9 +497,9 @@ cudaError_t wgrad(const void *dy, const void *x_codes, const void *x_scales, flo
                            k % 4 == 0 && (reinterpret_cast<uintptr_t>(dw) & 15) == 0 ? 1 : 0, status);
     if (e == cudaSuccess) e = cudaGetLastError();
   }
-  if (e != cudaSuccess || cut.pairs == 1) return e;
+  if (e != cudaSuccess || cut.rest == 0) return e;
   ProfScope ps("q8_wgrad_join", st);
-  wgrad_join_kernel<<<dim3((unsigned)(cut.units / cut.steps), kTn * kTk / 1024), 256, 0, st>>>(
+  wgrad_join_kernel<<<dim3((unsigned)cut.rest, kTn * kTk / 1024), 256, 0, st>>>(
       static_cast<const float *>(workspace), dw, cut, accumulate ? 1 : 0, n, k);
   return cudaGetLastError();
 }

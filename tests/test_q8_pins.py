@@ -173,7 +173,9 @@ def test_other_refusals(lib):
     assert c["matmul"](n=-1) == INVALID
     assert c["matmul"](cols=131073) == UNSUPPORTED
     assert c["wgrad"](dw=None) == INVALID
-    assert c["wgrad"](ws_bytes=16) == WORKSPACE
+    assert c["wgrad"](rows=4096, ws_bytes=16) == WORKSPACE
+    assert c["wgrad"](rows=4096, ws=None) == WORKSPACE
+    assert c["wgrad"](rows=4096, ws=vp(4096 + 4)) == UNSUPPORTED
     assert c["wgrad"](n=-1) == INVALID
 
 
