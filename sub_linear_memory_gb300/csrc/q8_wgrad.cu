@@ -43,15 +43,17 @@ constexpr int kPairs = 76;      // one CTA for each of 152 SMs
 constexpr int kTn = 256, kTk = 256, kStep = 64;  // a pair's tile and rows of a step
 constexpr int kMinSteps = 8;    // per pair: a partial tile costs about this much
 constexpr int kWindow = 20;     // steps in one accumulator
-constexpr int kThreads = 512;   // loads, MMA, tensor memory, scales; four converting, eight adding warps
-constexpr int kStages = 6, kBufs = 4;
+constexpr int kThreads = 512;   // loads, MMA, scales; four converting, eight adding warps
+// Two rings: dy with the converted tiles (freed together by the MMAs), and the
+// codes (freed by the converting warps).
+constexpr int kBufs = 5, kCodes = 6;
 constexpr uint32_t kDBytes = kStep * kBlock * 2, kCBytes = kStep * kBlock, kBBytes = kStep * kBlock * 2;
-constexpr uint32_t kStageBytes = kDBytes + kCBytes;
-constexpr uint32_t kTable = kStep * 8;  // factors of a step's rows
-constexpr uint32_t oB = kStages * kStageBytes, oTable = oB + kBufs * kBBytes, oBar = oTable + kStages * kTable;
+constexpr uint32_t kTable = kStep * 4;  // scale words of a step's rows
+constexpr uint32_t oB = kBufs * kDBytes, oCodes = oB + kBufs * kBBytes, oTable = oCodes + kCodes * kCBytes,
+                   oBar = oTable + kCodes * kTable;
 enum {
-  S_DY = 0, S_CODES = S_DY + kStages, S_EMPTY = S_CODES + kStages, S_BFULL = S_EMPTY + kStages,
-  S_BEMPTY = S_BFULL + kBufs, S_ACC = S_BEMPTY + kBufs, S_ACCFREE = S_ACC + 2, S_DONE = S_ACCFREE + 2, S_COUNT
+  S_DY = 0, S_BFULL = S_DY + kBufs, S_FREE = S_BFULL + kBufs, S_CODES = S_FREE + kBufs,
+  S_CODESFREE = S_CODES + kCodes, S_ACC = S_CODESFREE + kCodes, S_ACCFREE = S_ACC + 2, S_DONE = S_ACCFREE + 2, S_COUNT
 };
 constexpr uint32_t kSmem = 1024 + oBar + 512;
 
@@ -153,7 +155,7 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // 2^(120 + e) as a pair of equal bf16 numbers for a scale byte, in two factors
 // where it is past the type's range (e > 7); NaN for a NaN block.
 __device__ __forceinline__ uint32_t factor(int byte, uint32_t &second) {
-  second = 0;
+  second = 0;  // none
   if (byte == kScaleNan) return 0x7fff7fffu;
   const int e = byte - 127;
   const int first = min(120 + e, 127);  // e >= -127
@@ -164,6 +166,16 @@ __device__ __forceinline__ uint32_t factor(int byte, uint32_t &second) {
   const uint32_t f = (uint32_t)(first + 127) << 7;
   return f | (f << 16);
 }
+
+// Asynchronous copies of 4 bytes, tracked by an mbarrier: each lane's arrival
+// (part of the barrier's count) comes when its copies have landed.
+__device__ __forceinline__ void copy_async4(uint32_t to, const uint8_t *from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <bool TMA_DY>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -179,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1;
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar + S_DY + s, 1);
-      mbar_init(bar + S_CODES + s, 2);  // the loads and the scales
-      mbar_init(bar + S_EMPTY + s, 5);  // the MMAs and the converting warps
+    for (int s = 0; s < kCodes; ++s) {
+      mbar_init(bar + S_CODES + s, 1 + 32);  // the load and the scales' lanes
+      mbar_init(bar + S_CODESFREE + s, 2);  // two converting warps
     }
     for (int b = 0; b < kBufs; ++b) {
-      mbar_init(bar + S_BFULL + b, 8);  // converting warps of both CTAs
-      mbar_init(bar + S_BEMPTY + b, 1);
+      mbar_init(bar + S_DY + b, 1);
+      mbar_init(bar + S_BFULL + b, 4);  // two converting warps of each CTA
+      mbar_init(bar + S_FREE + b, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar + S_ACC + b, 1);
@@ -220,30 +232,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive_pair(map_peer(smem_u32(bar + b), 0));
   };
-  // Registers of the launch: 512 x 128.  The warpgroups' shares (56 + 96 + 2 x
-  // 176, times 128) come to 64512 of these 65536.
+  // Registers of the launch: 512 x 128.  The warpgroups' shares (64 + 96 + 2 x
+  // 176, times 128) come to these 65536.
   if (warp < 4) {
-    regs_dec<56>();
+    regs_dec<64>();
     if (warp == 0 && lane == 0) {
       int i = 0;
       for (Walk p(cut, pair, rank); p.more; p.next(), ++i) {
-        const int r0 = p.step * kStep;
-        const int s = i % kStages;
-        if (i >= kStages && !wait(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1)) break;
-        const uint32_t at = sbase + s * kStageBytes;
-        if (TMA_DY) {
-          if (rank == 0) mbar_arrive_expect_tx(bar + S_DY + s, 2 * kDBytes);
-          const uint32_t full = map_peer(smem_u32(bar + S_DY + s), 0);
-          tma_load_2d_pair(at, &mdy, full, p.n0, r0);
-          tma_load_2d_pair(at + kDBytes / 2, &mdy, full, p.n0 + 64, r0);
-        }
+        const int s = i % kCodes;
+        if (i >= kCodes && !wait(S_CODESFREE + s, (uint32_t)(i / kCodes - 1) & 1)) break;
         mbar_arrive_expect_tx(bar + S_CODES + s, kCBytes);
-        tma_load_2d(at + kDBytes, &mx, bar + S_CODES + s, p.blk * kBlock, r0);
+        tma_load_2d(sbase + oCodes + s * kCBytes, &mx, bar + S_CODES + s, p.blk * kBlock, p.step * kStep);
       }
-      for (int j = max(0, i - kStages); j < i; ++j) {
-        mbar_drain(bar + S_CODES + j % kStages, (uint32_t)(j / kStages) & 1);
-        if (TMA_DY && rank == 0) mbar_drain(bar + S_DY + j % kStages, (uint32_t)(j / kStages) & 1);
+      for (int j = max(0, i - kCodes); j < i; ++j) mbar_drain(bar + S_CODES + j % kCodes, (uint32_t)(j / kCodes) & 1);
+    } else if (warp == 2 && lane == 0 && TMA_DY) {
+      int i = 0;
+      for (Walk p(cut, pair, rank); p.more; p.next(), ++i) {
+        const int s = i % kBufs;
+        if (i >= kBufs && !wait(S_FREE + s, (uint32_t)(i / kBufs - 1) & 1)) break;
+        if (rank == 0) mbar_arrive_expect_tx(bar + S_DY + s, 2 * kDBytes);
+        const uint32_t full = map_peer(smem_u32(bar + S_DY + s), 0), at = sbase + s * kDBytes;
+        tma_load_2d_pair(at, &mdy, full, p.n0, p.step * kStep);
+        tma_load_2d_pair(at + kDBytes / 2, &mdy, full, p.n0 + 64, p.step * kStep);
       }
+      if (rank == 0)
+        for (int j = max(0, i - kBufs); j < i; ++j) mbar_drain(bar + S_DY + j % kBufs, (uint32_t)(j / kBufs) & 1);
     } else if (warp == 1 && rank == 0) {
       const bool issues = elect_lane();
       const uint32_t id = make_idesc(kTn, kTk, true, true);
@@ -256,20 +269,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t acc = tbase + (win & 1) * kTk;
           const int end = min(first + kWindow, seg.s1);
           for (int step = first; step < end; ++step, ++i) {
-            const int s = i % kStages, b = i % kBufs;
-            if (TMA_DY && !wait_warp(S_DY + s, (uint32_t)(i / kStages) & 1)) break;
+            const int b = i % kBufs;
+            if (TMA_DY && !wait_warp(S_DY + b, (uint32_t)(i / kBufs) & 1)) break;
             if (!wait_warp(S_BFULL + b, (uint32_t)(i / kBufs) & 1)) break;
             tc_fence_after();
-            const uint64_t da = desc_mnmajor(sbase + s * kStageBytes, kStep, 0, 0);
+            const uint64_t da = desc_mnmajor(sbase + b * kDBytes, kStep, 0, 0);
             const uint64_t db = desc_mnmajor(sbase + oB + b * kBBytes, kStep, 0, 0);
 #pragma unroll
             for (int j = 0; j < kStep / 16; ++j)
               if (issues)
                 mma_bf16_pair(acc, da + (uint64_t)(j * 128), db + (uint64_t)(j * 128), id, step > first || j > 0);
-            if (issues) {
-              mma_commit_pair(bar + S_EMPTY + s);
-              mma_commit_pair(bar + S_BEMPTY + b);
-            }
+            if (issues) mma_commit_pair(bar + S_FREE + b);
             __syncwarp();
           }
           if (ok && issues) mma_commit_pair(bar + S_ACC + (win & 1));
@@ -280,96 +290,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_drain(bar + S_DONE, 0);
     } else if (warp == 3) {
-      // Factors of each step's rows, two rows a lane.  Four steps' scale bytes
-      // are on their way from memory while one step's are stored.
-      constexpr int kAhead = 4;
-      int byte[kAhead][2];
-      Walk p(cut, pair, rank);
-      auto fetch = [&](int (&v)[2]) {  // steps in order; -1 past the last
+      // The scale words of each step's rows, two rows a lane, copied without
+      // passing through registers: the copies' own arrivals complete the
+      // barrier, so this warp is as far ahead as the codes.  (Loading the bytes
+      // four steps ahead into registers held a step to 930 cycles.)
+      int i = 0;
+      for (Walk p(cut, pair, rank); p.more && ok; p.next(), ++i) {
+        const int s = i % kCodes;
+        if (i >= kCodes && !wait_warp(S_CODESFREE + s, (uint32_t)(i / kCodes - 1) & 1)) break;
+        const uint32_t to = sbase + oTable + s * kTable;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = p.step * kStep + lane + 32 * h;
-          v[h] = !p.more                                ? -1
-                 : r < rows && p.blk * kBlock < k ? (int)__ldg(scales + (size_t)r * pitch + p.blk)
-                                                        : 127;
+          if (r < rows && p.blk * kBlock < k)
+            copy_async4(to + (lane + 32 * h) * 4, scales + (size_t)r * pitch + (p.blk & ~3));
         }
-        if (p.more) p.next();
-      };
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) fetch(byte[a]);
-      for (int i0 = 0; byte[0][0] >= 0 && ok; i0 += kAhead) {
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          const int i = i0 + a, s = i % kStages;
-          if (byte[a][0] >= 0 && ok && (i < kStages || wait_warp(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1))) {
-            uint2 *table = reinterpret_cast<uint2 *>(smem + oTable + s * kTable);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint2 f;
-              f.x = factor(byte[a][h], f.y);
-              table[lane + 32 * h] = f;
-            }
-            arrive(S_CODES + s);
-            fetch(byte[a]);
-          }
-        }
+        copy_async_arrive(bar + S_CODES + s);
       }
+      copy_async_wait();
     }
   } else if (warp < 8) {
     regs_dec<96>();
-    // thread: 16 codes of rows row0 + 16 j
-    const int ct = tid - 128, chunk = ct & 7, row0 = ct >> 3;
-    int i = 0;
-    for (Walk p(cut, pair, rank); p.more && ok; p.next(), ++i) {
-      const int s = i % kStages, b = i % kBufs;
-      if (!wait(S_CODES + s, (uint32_t)(i / kStages) & 1)) break;
-      uint4 code[4];
-      uint2 f[4];
-      const uint32_t from = sbase + s * kStageBytes + kDBytes + chunk * 16;
-      const uint2 *table = reinterpret_cast<const uint2 *>(smem + oTable + s * kTable);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ld_shared_v4(from + (row0 + 16 * j) * kBlock, code[j].x, code[j].y, code[j].z, code[j].w);
-        f[j] = table[row0 + 16 * j];
-      }
-      if (!TMA_DY) {  // rows that TMA cannot step over: these warps load them into the same layout
+    // Two warps convert a step, the other two the next: what a step costs
+    // besides its arithmetic (waits, the proxy fence, arrivals) overlaps.
+    // Thread: 16 codes of rows row0 + 8 j.
+    const int chunk = lane & 7, row0 = 4 * (warp & 1) + (lane >> 3);
+    // A thread's two 16-byte stores, in an order that keeps eight lanes on
+    // distinct banks: the right four of them begin with the second half.
+    const bool swap = chunk & 4;
+    Walk p(cut, pair, rank);
+    for (int i = 0; p.more && ok; p.next(), ++i) {
+      if ((i & 1) != ((warp >> 1) & 1)) continue;
+      const int s = i % kCodes, b = i % kBufs;
+      if (i >= kBufs && !wait_warp(S_FREE + b, (uint32_t)(i / kBufs - 1) & 1)) break;
+      if (!TMA_DY) {  // rows that TMA cannot step over: loaded here into the same layout
         const int r0 = p.step * kStep;
-        for (int x = ct; x < kStep * kBlock; x += 128) {
+        for (int x = 32 * (warp & 1) + lane; x < kStep * kBlock; x += 64) {
           const int r = x / kBlock, c = x % kBlock;
           const __nv_bfloat16 v =
               r0 + r < rows && p.n0 + c < n ? dy[(size_t)(r0 + r) * n + p.n0 + c] : __float2bfloat16_rn(0.f);
-          *reinterpret_cast<__nv_bfloat16 *>(smem + s * kStageBytes + sw128_offset(r, c, kStep)) = v;
+          *reinterpret_cast<__nv_bfloat16 *>(smem + b * kDBytes + sw128_offset(r, c, kStep)) = v;
         }
       }
-      if (i >= kBufs && !wait(S_BEMPTY + b, (uint32_t)(i / kBufs - 1) & 1)) break;
-      const uint32_t to = sbase + oB + b * kBBytes;
+      if (!wait_warp(S_CODES + s, (uint32_t)(i / kCodes) & 1)) break;
+      const uint32_t from = sbase + oCodes + s * kCBytes + chunk * 16, to = sbase + oB + b * kBBytes;
+      // factor of one row a lane (row 4 (warp & 1) + lane % 4 + 8 (lane / 4))
+      const int mine = 4 * (warp & 1) + (lane & 3) + 8 * (lane >> 2);
+      int byte = 127;
+      if (p.step * kStep + mine < rows && p.blk * kBlock < k)
+        byte = smem[oTable + s * kTable + mine * 4 + (p.blk & 3)];
+      uint32_t second;
+      const uint32_t first = factor(byte, second);
+      const bool twice = __any_sync(0xffffffffu, second != 0);
+      if (second == 0) second = 0x3f803f80u;  // one, for the rows that need none
+      // all loads first: each store after them would hold the next load back
+      uint32_t x[kStep / 8][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+      for (int j = 0; j < kStep / 8; ++j) {
+        ld_shared_v4(from + (row0 + 8 * j) * kBlock, x[j][0], x[j][1], x[j][2], x[j][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < kStep / 8; ++j) {
+        const int r = row0 + 8 * j;
+        const uint32_t w[4] = {swap ? x[j][2] : x[j][0], swap ? x[j][3] : x[j][1], swap ? x[j][0] : x[j][2],
+                               swap ? x[j][1] : x[j][3]};
+        const uint32_t f = __shfl_sync(0xffffffffu, first, 4 * j + (lane >> 3));
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          o[2 * e] = mul_bf16x2(widen(w[e], 0x1404), f[j].x);
-          o[2 * e + 1] = mul_bf16x2(widen(w[e], 0x3424), f[j].x);
+          o[2 * e] = mul_bf16x2(widen(w[e], 0x1404), f);
+          o[2 * e + 1] = mul_bf16x2(widen(w[e], 0x3424), f);
         }
-        if (f[j].y) {
+        if (twice) {
+          const uint32_t g = __shfl_sync(0xffffffffu, second, 4 * j + (lane >> 3));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f[j].y);
+          for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], g);
         }
-        // the two 16-byte halves in an order that keeps eight lanes on distinct banks
-        const int r = row0 + 16 * j;
-        const uint32_t a0 = to + sw128_offset(r, 16 * chunk, kStep), a1 = to + sw128_offset(r, 16 * chunk + 8, kStep);
-        if (chunk & 4) {
-          st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-          st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-        } else {
-          st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-          st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-        }
+        const uint32_t at = to + sw128_offset(r, 16 * chunk, kStep) ^ (swap ? 16u : 0u);
+        st_shared_v4(at, o[0], o[1], o[2], o[3]);
+        st_shared_v4(at ^ 16u, o[4], o[5], o[6], o[7]);
       }
       fence_async_smem();
       arrive_leader(S_BFULL + b);
-      arrive(S_EMPTY + s);
+      arrive(S_CODESFREE + s);
     }
   } else {
     regs_inc<176>();
