@@ -3,9 +3,9 @@
 //
 // The sum runs over rows, across which the scales of x differ, so the tensor
 // cores cannot apply them; but code * 2^e is exactly a bf16 number, and dy is
-// bf16.  Four warps turn each tile of codes into bf16 in shared memory (a
-// shift, two masks and one packed multiply for two codes) while the tensor
-// cores (kind::f16, both operands MN-major) work on the tiles before.
+// bf16.  Four warps turn each tile of codes into bf16 in shared memory (shifts,
+// masks and a packed multiply) while the tensor cores (kind::f16, both operands
+// MN-major) work on the tiles before.
 //
 // Tile: a CTA pair (cta_group::2) forms 256 (n) x 256 (k), each CTA loading
 // 128 columns of dy and converting one 128-column block of x, so that a code
@@ -137,14 +137,20 @@ struct Walk {
   }
 };
 
-// Two e4m3 codes in bytes 0 and 1 (or 2 and 3) of w as bf16 bits: sign and the
-// seven bits moved to the top of exponent and fraction, i.e. the value times
-// 2^-120 (the exponent biases are 7 and 127; subnormal codes become subnormal
-// bf16 numbers).
-__device__ __forceinline__ uint32_t widen(uint32_t w, uint32_t sel) {
-  const uint32_t t = __byte_perm(w, 0, sel);  // a code in the high byte of each half
-  return ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+// Four e4m3 codes c0..c3 as bf16 bits, (c0, c2) and (c1, c3): sign, and the
+// seven other bits at the bottom of the exponent and the top of the fraction,
+// i.e. the value times 2^-120 (the exponent biases are 7 and 127; subnormal
+// codes become subnormal bf16 numbers).  Taking alternate codes needs no byte
+// permutation, and the left shifts are multiplications, so that the integer
+// pipe, which bounds the conversion, has five operations for four codes (with
+// a permutation for each pair it had eight, and a step took 1030 cycles).
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &even, uint32_t &odd) {
+  even = ((w * 16u) & 0x07f007f0u) | ((w * 256u) & 0x80008000u);
+  odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
 }
+// The columns of a converted tile are therefore x's in the order 0 2 1 3 of
+// each four; the accumulator's columns 4 q + 1 and 4 q + 2 change places when
+// the result is written.
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -165,6 +171,10 @@ __device__ __forceinline__ uint32_t factor(int byte, uint32_t &second) {
   }
   const uint32_t f = (uint32_t)(first + 127) << 7;
   return f | (f << 16);
+}
+
+__device__ __forceinline__ void ld_shared_v2(uint32_t addr, uint32_t &a, uint32_t &b) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 
 // Asynchronous copies of 4 bytes, tracked by an mbarrier: each lane's arrival
@@ -315,9 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // besides its arithmetic (waits, the proxy fence, arrivals) overlaps.
     // Thread: 16 codes of rows row0 + 8 j.
     const int chunk = lane & 7, row0 = 4 * (warp & 1) + (lane >> 3);
-    // A thread's two 16-byte stores, in an order that keeps eight lanes on
-    // distinct banks: the right four of them begin with the second half.
-    const bool swap = chunk & 4;
+    // A thread's two 8-byte loads and two 16-byte stores of a row, in an order
+    // that keeps the lanes served together on distinct banks: half of them
+    // begin with the second half.
+    const bool swap = ((chunk >> 2) ^ (lane >> 3)) & 1;
     Walk p(cut, pair, rank);
     for (int i = 0; p.more && ok; p.next(), ++i) {
       if ((i & 1) != ((warp >> 1) & 1)) continue;
@@ -334,6 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!wait_warp(S_CODES + s, (uint32_t)(i / kCodes) & 1)) break;
       const uint32_t from = sbase + oCodes + s * kCBytes + chunk * 16, to = sbase + oB + b * kBBytes;
+      // Everything that waits for memory or for other lanes comes before the
+      // arithmetic: between the stores, which keep their order, each shuffle
+      // and load would wait for its turn.
+      uint32_t x[kStep / 8][4], f[kStep / 8];
+#pragma unroll
+      for (int j = 0; j < kStep / 8; ++j) {
+        const uint32_t at = from + (row0 + 8 * j) * kBlock;
+        ld_shared_v2(at ^ (swap ? 8u : 0u), x[j][0], x[j][1]);
+        ld_shared_v2(at ^ (swap ? 0u : 8u), x[j][2], x[j][3]);
+      }
       // factor of one row a lane (row 4 (warp & 1) + lane % 4 + 8 (lane / 4))
       const int mine = 4 * (warp & 1) + (lane & 3) + 8 * (lane >> 2);
       int byte = 127;
@@ -343,23 +364,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t first = factor(byte, second);
       const bool twice = __any_sync(0xffffffffu, second != 0);
       if (second == 0) second = 0x3f803f80u;  // one, for the rows that need none
-      // all loads first: each store after them would hold the next load back
-      uint32_t x[kStep / 8][4];
 #pragma unroll
-      for (int j = 0; j < kStep / 8; ++j) {
-        ld_shared_v4(from + (row0 + 8 * j) * kBlock, x[j][0], x[j][1], x[j][2], x[j][3]);
-      }
+      for (int j = 0; j < kStep / 8; ++j) f[j] = __shfl_sync(0xffffffffu, first, 4 * j + (lane >> 3));
 #pragma unroll
       for (int j = 0; j < kStep / 8; ++j) {
         const int r = row0 + 8 * j;
-        const uint32_t w[4] = {swap ? x[j][2] : x[j][0], swap ? x[j][3] : x[j][1], swap ? x[j][0] : x[j][2],
-                               swap ? x[j][1] : x[j][3]};
-        const uint32_t f = __shfl_sync(0xffffffffu, first, 4 * j + (lane >> 3));
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          o[2 * e] = mul_bf16x2(widen(w[e], 0x1404), f);
-          o[2 * e + 1] = mul_bf16x2(widen(w[e], 0x3424), f);
+          widen4(x[j][e], o[2 * e], o[2 * e + 1]);
+          o[2 * e] = mul_bf16x2(o[2 * e], f[j]);
+          o[2 * e + 1] = mul_bf16x2(o[2 * e + 1], f[j]);
         }
         if (twice) {
           const uint32_t g = __shfl_sync(0xffffffffu, second, 4 * j + (lane >> 3));
@@ -400,6 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive_leader(S_ACCFREE + (win & 1));
       }
       if (!ok) break;
+#pragma unroll
+      for (int e = 0; e < 128; e += 4) {  // the columns' own order
+        const float u = sum[e + 1];
+        sum[e + 1] = sum[e + 2];
+        sum[e + 2] = u;
+      }
       // into dw, or into this pair's partial tile
       const int n0 = seg.tile / cut.tiles_k * kTn, kk = seg.tile % cut.tiles_k * kTk + c0;
       float *to = whole ? dw + (size_t)(n0 + nr) * k + kk
