@@ -21,6 +21,8 @@ cudaError_t gelu_bwd(const void *da, const void *z_codes, const void *z_scales, 
 template <typename T>
 cudaError_t pack_weight(const void *w, void *codes, void *scales, void *codes_t, void *scales_t, int n, int k,
                         cudaStream_t st);
+
+// q8_norm.cu
 template <typename T>
 cudaError_t rms_norm(const void *x, const void *res, const float *gamma, float eps, void *h, float *rstd,
                      void *y_codes, void *y_scales, void *h_codes, void *h_scales, int rows, int cols,

@@ -4,6 +4,8 @@
 
 #include <cuda_fp8.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 
 namespace slim {
@@ -97,42 +99,46 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float *v) {
   }
 }
 
-// 8 consecutive columns of a row, `left` of them inside it (the rest are 0).
-// VEC: the row is aligned and left is 8 or <= 0.  Plain loads, not the
-// read-only path: outputs may be the inputs' own buffers.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, int left, float *v);
+// 8 consecutive columns of a row as they lie in memory, `left` of them inside it
+// (the rest are 0).  VEC: the row is aligned and left is 8 or <= 0.  Plain
+// loads, not the read-only path: outputs may be the inputs' own buffers.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> { uint4 w; };
+template <> struct Raw8<float> { float4 a, b; };
 
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16, true>(const __nv_bfloat16 *p, int left, float *v) {
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (left > 0) w = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T> load_raw8(const T *p, int left) {
+  if constexpr (!VEC) {
+    T v[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = i < left ? p[i] : from_f32<T>(0.f);
+    Raw8<T> r;
+    memcpy(&r, v, sizeof(r));
+    return r;
+  } else if constexpr (sizeof(T) == 2) {
+    return Raw8<T>{left > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0)};
+  } else {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    return left > 0 ? Raw8<T>{reinterpret_cast<const float4 *>(p)[0], reinterpret_cast<const float4 *>(p)[1]}
+                    : Raw8<T>{z, z};
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16> &r, float *v) {
+  const uint32_t u[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(u[i] << 16);
     v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
-template <>
-__device__ __forceinline__ void load8<float, true>(const float *p, int left, float *v) {
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-  if (left > 0) {
-    a = reinterpret_cast<const float4 *>(p)[0];
-    b = reinterpret_cast<const float4 *>(p)[1];
-  }
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void unpack8(const Raw8<float> &r, float *v) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16, false>(const __nv_bfloat16 *p, int left, float *v) {
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.f;
-}
-template <>
-__device__ __forceinline__ void load8<float, false>(const float *p, int left, float *v) {
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) v[i] = i < left ? p[i] : 0.f;
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T *p, int left, float *v) {
+  unpack8(load_raw8<T, VEC>(p, left), v);
 }
 
 template <typename T, bool VEC>
@@ -166,6 +172,14 @@ __device__ __forceinline__ void store8<float, false>(float *p, int left, const f
 #pragma unroll
   for (int i = 0; i < kVec; ++i)
     if (i < left) p[i] = v[i];
+}
+
+// 16-byte accesses of 8 columns: every row starts on 16 bytes.
+inline bool vector_rows(int cols, std::initializer_list<const void *> ptrs) {
+  if (cols % kVec) return false;
+  for (const void *p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return true;
 }
 
 // What a value becomes when it is stored as T.
