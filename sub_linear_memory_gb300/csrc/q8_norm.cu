@@ -43,15 +43,17 @@ template <int W> struct NormCfg {
 };
 
 // How many CTAs share an SM: their rows' loads are what hides the memory's
-// latency.  (With the 193 registers that an unbounded bf16 backward took, one
-// CTA was left and 65536 x 1024 took 296 us.)
-template <typename T, int W> constexpr int norm_ctas() { return W > 8 || sizeof(T) == 4 ? 1 : 2; }
+// latency.  Forward, 65536 x 1024 bf16: 121 us with two, 97 with three, 90 with
+// four; fp32 145, 141, 151.  Backward: two (one was left with the 193
+// registers that bf16 took unbounded: 296 us, 103 with two), and one for fp32.
+template <typename T, int W> constexpr int fwd_ctas() { return W > 8 ? 2 : sizeof(T) == 2 ? 4 : 3; }
+template <typename T, int W> constexpr int bwd_ctas() { return W > 8 || sizeof(T) == 4 ? 1 : 2; }
 
 // W warps hold a row, each thread NC chunks of 8 of its columns, in registers
 // between the sum of squares and the quantization: h and y are formed from one
 // read of x and res.
 template <typename T, int W, int NC, bool VEC>
-__global__ void __launch_bounds__(NormCfg<W>::kThreads, norm_ctas<T, W>())
+__global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
     rms_norm_kernel(const T *x, const T *res, const float *gamma, float eps, T *h, float *rstd, Mat8 y, Mat8 hq,
                     Shape8 s) {
   __shared__ float part[NormCfg<W>::kThreads / 32];
@@ -93,9 +95,11 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, norm_ctas<T, W>())
   const float root = 1.f / sqrtf(m);
   if (rstd && live && l == 0) rstd[row] = root;
   // What the rounding of root left out, by one Newton step.  y is formed with
-  // it and with the roundings of its first product, so that an e4m3 code
+  // it and with the rounding of its first product, so that an e4m3 code
   // differs from the exact y's only where that lies within 2^-24 of a border.
-  const float rest = root < INFINITY ? 0.5f * root * fmaf(-m * root, root, 1.f) : 0.f;
+  // (Where a product overflows the remainder is NaN, and so is the block.)
+  const float rest = m < INFINITY && root < INFINITY ? 0.5f * root * fmaf(-m * root, root, 1.f) : 0.f;
+  const float2 root2 = make_float2(root, root), rest2 = make_float2(rest, rest);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int chunk = c * 32 * W + l, blk = chunk / kVecs, col = chunk * kVec;
@@ -104,12 +108,14 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, norm_ctas<T, W>())
     float g[kVec];
     load8<float, VEC>(gamma + col, s.cols - col, g);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float n = v[c][i] * root;
-      const float lost = fmaf(v[c][i], rest, fmaf(v[c][i], root, -n));
-      const float full = fmaf(n, g[i], lost * g[i]);
-      // an infinity has no remainder (inf - inf); columns past the row are 0 whatever root is
-      v[c][i] = col + i < s.cols ? (fabsf(n) < INFINITY ? full : n * g[i]) : 0.f;
+    for (int i = 0; i < kVec; i += 2) {
+      const float2 x = make_float2(v[c][i], v[c][i + 1]), gg = make_float2(g[i], g[i + 1]);
+      const float2 n = __fmul2_rn(x, root2);
+      const float2 lost = __ffma2_rn(x, rest2, __ffma2_rn(x, root2, make_float2(-n.x, -n.y)));
+      const float2 full = __ffma2_rn(n, gg, __fmul2_rn(lost, gg));
+      // columns past the row are 0 whatever root is
+      v[c][i] = (VEC ? col : col + i) < s.cols ? full.x : 0.f;
+      v[c][i + 1] = (VEC ? col : col + i + 1) < s.cols ? full.y : 0.f;
     }
     put_block8(v[c], y, s, row, blk, lane16, on);
   }
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, norm_ctas<T, W>())
 constexpr int kBwdCtas = 304;  // two for each of 152 SMs: fixed, so that the order of the sums is
 
 template <typename T, int W, int NC, bool VEC, bool KEPT8>
-__global__ void __launch_bounds__(NormCfg<W>::kThreads, norm_ctas<T, W>())
+__global__ void __launch_bounds__(NormCfg<W>::kThreads, bwd_ctas<T, W>())
     rms_norm_bwd_kernel(const T *dy, const T *h, const uint8_t *hc, const uint8_t *hs, const float *rstd,
                         const float *gamma, const T *dres, T *dh, float *partial, Shape8 s) {
   extern __shared__ float columns[];
@@ -295,14 +301,14 @@ cudaError_t rms_norm(const void *x, const void *res, const float *gamma, float e
   return cudaGetLastError();
 }
 
-static int bwd_ctas(int rows, int cols) {
+static int bwd_grid(int rows, int cols) {
   int per = 1;
   with_width(cols, [&](auto w, auto) { per = NormCfg<decltype(w)::value>::kRows; });
   return (int)std::min<long long>(kBwdCtas, ((long long)rows + per - 1) / per);
 }
 
 size_t rms_norm_bwd_workspace(int rows, int cols) {
-  return (size_t)bwd_ctas(rows, cols) * blocks_of(cols) * kBlock * sizeof(float);
+  return (size_t)bwd_grid(rows, cols) * blocks_of(cols) * kBlock * sizeof(float);
 }
 
 template <typename T>
@@ -315,7 +321,7 @@ cudaError_t rms_norm_bwd(const void *dy, const void *h, const void *h_codes, con
   T *out = static_cast<T *>(dh);
   float *partial = dgamma ? static_cast<float *>(workspace) : nullptr;
   const bool vec = vector_rows(cols, {dy, h, dres, dh, gamma});
-  const int ctas = bwd_ctas(rows, cols);
+  const int ctas = bwd_grid(rows, cols);
   if (ctas > 0) {
     ProfScope ps("q8_rms_norm_bwd", st);
     with_width(cols, [&](auto w, auto nc) {

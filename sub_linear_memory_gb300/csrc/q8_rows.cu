@@ -17,6 +17,12 @@ using tc::ex2_ftz;
 
 // ---- GeLU -------------------------------------------------------------------
 
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The normal distribution function and density at two points.  The tail
 // beyond |z| is exp(-z^2 / 2) times a polynomial in u = 1 / (1 + 0.35 |z|) (the
 // form of Hastings, Approximations for Digital Computers, 1955), of degree 9
@@ -28,7 +34,7 @@ using tc::ex2_ftz;
 __device__ __forceinline__ void normal_parts(float2 z, float2 &cdf, float2 &pdf) {
   const float2 t = make_float2(fabsf(z.x), fabsf(z.y));
   const float2 d = __ffma2_rn(t, make_float2(0.35f, 0.35f), make_float2(1.f, 1.f));
-  const float2 u = make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y));
+  const float2 u = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
   float2 p = make_float2(-0.029146051f, -0.029146051f);
   auto step = [&](float c) { p = __ffma2_rn(p, u, make_float2(c, c)); };
   step(0.14397228f);
@@ -49,12 +55,12 @@ __device__ __forceinline__ void normal_parts(float2 z, float2 &cdf, float2 &pdf)
 
 // ---- elementwise over blocks of 128 columns -----------------------------------
 
-constexpr int kEltThreads = 256, kEltUnroll = 4;
+constexpr int kEltThreads = 256, kEltUnroll = 4, kEltCtas = 4;
 
 // GELU: a = 8 bits of GeLU(x), z (where wanted) = 8 bits of x; otherwise
 // a = 8 bits of x.
 template <typename T, bool GELU, bool VEC>
-__global__ void __launch_bounds__(kEltThreads) quantize_kernel(const T *x, Mat8 a, Mat8 z, Shape8 s,
+__global__ void __launch_bounds__(kEltThreads, kEltCtas) quantize_kernel(const T *x, Mat8 a, Mat8 z, Shape8 s,
                                                                unsigned blocks) {
   const int lane16 = threadIdx.x & (kVecs - 1);
   const unsigned first = blockIdx.x * (unsigned)(kEltThreads / kVecs * kEltUnroll) + threadIdx.x / kVecs;
@@ -87,7 +93,7 @@ __global__ void __launch_bounds__(kEltThreads) quantize_kernel(const T *x, Mat8 
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kEltThreads) dequantize_kernel(const uint8_t *codes, const uint8_t *scales, T *x,
+__global__ void __launch_bounds__(kEltThreads, kEltCtas) dequantize_kernel(const uint8_t *codes, const uint8_t *scales, T *x,
                                                                  Shape8 s, int row_shift, unsigned blocks) {
   const int lane16 = threadIdx.x & (kVecs - 1);
   const unsigned first = blockIdx.x * (unsigned)(kEltThreads / kVecs * kEltUnroll) + threadIdx.x / kVecs;
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kEltThreads) dequantize_kernel(const uint8_t *
 
 // dz = da (Phi(z) + z phi(z)) at the checkpointed z, and the 8 bits of dz.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kEltThreads) gelu_bwd_kernel(const T *da, const uint8_t *codes,
+__global__ void __launch_bounds__(kEltThreads, kEltCtas) gelu_bwd_kernel(const T *da, const uint8_t *codes,
                                                                const uint8_t *scales, T *dz, Mat8 q, Shape8 s,
                                                                unsigned blocks) {
   const int lane16 = threadIdx.x & (kVecs - 1);
