@@ -43,7 +43,7 @@ template <bool F32>
 __global__ void __launch_bounds__(kThreads)
     matmul_small_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ma,
                         const uint8_t *a_scales, const uint8_t *b_scales, void *out, int rows, int n, int kb,
-                        int pitch, int nt, int *status) {
+                        int pitch, int nt, int wide, int *status) {
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t sbase = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t *smem = raw + (sbase - smem_u32(raw));
@@ -159,15 +159,44 @@ __global__ void __launch_bounds__(kThreads)
   __syncwarp();
   if (split > 1) {
     cluster_sync();
-    const int cols = min(nt, rows - m0), nl = tid & (kBlock - 1);
+    // Four neighbouring columns of out a thread; a CTA takes every split-th
+    // group of 8 rows.  All loads of a group are under way together: they cross
+    // the SMs, and one after the other took most of the kernel (12.3 us for 128
+    // rows x 4096 x 1024).
+    const int cols = min(nt, rows - m0), nl = 4 * lane, left = n - n0 - nl;
     const uint32_t mine = smem_u32(part);
-    if (!*abort_flag && n0 + nl < n) {
-      for (int c = rank + split * (tid >> 7); c < cols; c += 2 * split) {
-        float x = 0.f;
-        for (int r = 0; r < split; ++r) x += ld_peer_f32(map_peer(mine + (uint32_t)(c * kBlock + nl) * 4u, r));
+    if (!*abort_flag && left > 0) {
+      for (int c = 8 * rank + warp; c < cols; c += 8 * split) {
+        float v[8][4];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < split) ld_peer_v4(map_peer(mine + (uint32_t)(c * kBlock + nl) * 4u, r), v[r]);
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < split) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[0][e] += v[r][e];
+          }
         const size_t at = (size_t)(m0 + c) * n + n0 + nl;
-        if (F32) static_cast<float *>(out)[at] = x;
-        else static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(x);
+        if (F32) {
+          float *to = static_cast<float *>(out) + at;
+          if (wide) {
+            *reinterpret_cast<float4 *>(to) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < left) to[e] = v[0][e];
+          }
+        } else {
+          __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(out) + at;
+          if (wide) {
+            *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < left) to[e] = __float2bfloat16_rn(v[0][e]);
+          }
+        }
       }
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
@@ -191,6 +220,8 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
   if (!make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, n, kp, kp, kBlock, kBlock, true) ||
       !make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, rows, kp, kp, nt, kBlock, true))
     return cudaErrorInvalidValue;
+  // four columns of out in one store
+  const int wide = n % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (F32 ? 15 : 7)) == 0;
   auto kern = matmul_small_kernel<F32>;
   const uint32_t smem = smem_bytes(nt, split > 1);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kBlock, true));
@@ -209,7 +240,7 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
   cfg.numAttrs = 1;
   ProfScope ps("q8_matmul_small", st);
   e = cudaLaunchKernelEx(&cfg, kern, mw, ma, static_cast<const uint8_t *>(a_scales),
-                         static_cast<const uint8_t *>(b_scales), out, rows, n, kb, scale_pitch(k), nt, status);
+                         static_cast<const uint8_t *>(b_scales), out, rows, n, kb, scale_pitch(k), nt, wide, status);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -139,10 +139,10 @@ __device__ __forceinline__ void tmem_st4u(uint32_t taddr, uint32_t a, uint32_t b
                : "memory");
 }
 
-__device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void ld_peer_v4(uint32_t addr, float *v) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr));
 }
 
 }  // namespace q8

@@ -69,25 +69,28 @@ class Q8(NamedTuple):
 
 def empty(rows, cols, block_rows=1, device=None):
     """An uninitialised Q8 of the given size."""
-    nb = -(-cols // BLOCK)
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    codes = torch.empty((rows, nb * BLOCK), dtype=torch.float8_e4m3fn, device=dev)
-    scales = torch.empty((-(-rows // block_rows), -(-nb // 4) * 4), dtype=torch.uint8, device=dev)
-    return Q8(codes, scales, cols, block_rows)
+    nb = -(-cols // BLOCK)
+    return Q8(torch.empty((rows, nb * BLOCK), dtype=torch.float8_e4m3fn, device=dev),
+              torch.empty((-(-rows // block_rows), -(-nb // 4) * 4), dtype=torch.uint8, device=dev), cols, block_rows)
+
+
+def _stream(device):
+    # the stream's handle alone: torch.cuda.current_stream builds an object around it, for more
+    # than a small kernel's launch costs
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+_TYPES = (torch.bfloat16, torch.float32)
 
 
 def _rows(t, what, like=None):
     """A dense CUDA bf16 or fp32 matrix; like: one of the same shape, type and device."""
-    if t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32) or t.device.type != "cuda" \
-            or not t.is_contiguous():
+    if t.dtype not in _TYPES or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA bf16 or fp32 [rows, cols] tensor" % what)
     if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
         raise ValueError("%s must have the other rows' shape, dtype and device" % what)
@@ -104,17 +107,22 @@ def _mat(q, what, block_rows=1, rows=None, cols=None, device=None):
     if q.block_rows != block_rows or q.codes.dtype != torch.float8_e4m3fn or q.scales.dtype != torch.uint8 \
             or q.codes.shape != (r, nb * BLOCK) or q.scales.shape != (-(-r // block_rows), -(-nb // 4) * 4) \
             or not q.codes.is_contiguous() or not q.scales.is_contiguous() or q.scales.device != q.codes.device \
-            or q.codes.device.type != "cuda":
+            or not q.codes.is_cuda:
         raise ValueError("%s must be a Q8 with one scale for each %d row(s) and 128 columns" % (what, block_rows))
     if (rows is not None and r != rows) or (cols is not None and q.cols != cols) \
             or (device is not None and q.codes.device != device):
         raise ValueError("%s does not have the other arguments' sizes and device" % what)
 
 
+_functions = {(_name, _dtype): (getattr(_lib, _name + _suffix), _name + _suffix)
+              for _name in _SIGNATURES for _dtype, _suffix in ((torch.bfloat16, ""), (torch.float32, "_f32"))}
+
+
 def _call(name, dtype, *args):
-    if dtype == torch.float32:
-        name += "_f32"
-    binding._check(getattr(_lib, name)(*args), name)
+    fn, what = _functions[name, dtype]
+    code = fn(*args)
+    if code:
+        raise binding.SlimError(code, what)
 
 
 def quantize(x, out=None):
@@ -123,8 +131,9 @@ def quantize(x, out=None):
     rows, cols = x.shape
     if out is None:
         out = empty(rows, cols, device=x.device)
-    _mat(out, "out", 1, rows, cols, x.device)
-    _call("slim_q8_quantize", x.dtype, x.data_ptr(), out.codes.data_ptr(), out.scales.data_ptr(), rows, cols, _stream(x))
+    else:
+        _mat(out, "out", 1, rows, cols, x.device)
+    _call("slim_q8_quantize", x.dtype, x.data_ptr(), out.codes.data_ptr(), out.scales.data_ptr(), rows, cols, _stream(x.device))
     return out
 
 
@@ -133,11 +142,11 @@ def dequantize(q, dtype=torch.bfloat16, out=None):
     _mat(q, "q", q.block_rows if q.block_rows in (1, BLOCK) else 1)
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    _rows(out, "out")
-    if out.shape != (q.rows, q.cols) or out.device != q.codes.device:
+    elif out.shape != (q.rows, q.cols) or out.device != q.codes.device:
         raise ValueError("out must be [rows, cols] on q's device")
+    _rows(out, "out")
     _call("slim_q8_dequantize", out.dtype, q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), q.rows, q.cols,
-          q.block_rows, _stream(out))
+          q.block_rows, _stream(out.device))
     return out
 
 
@@ -149,7 +158,7 @@ def pack_weight(w, transpose=True):
     q = empty(n, k, BLOCK, w.device)
     qt = empty(k, n, BLOCK, w.device) if transpose else None
     _call("slim_q8_pack_weight", w.dtype, w.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(),
-          _ptr(qt and qt.codes), _ptr(qt and qt.scales), n, k, _stream(w))
+          _ptr(qt and qt.codes), _ptr(qt and qt.scales), n, k, _stream(w.device))
     return q, qt
 
 
@@ -171,7 +180,7 @@ def rms_norm(x, gamma, res=None, eps=1e-5, checkpoint=False):
     h8 = empty(rows, cols, device=x.device) if checkpoint else None
     _call("slim_q8_rms_norm", x.dtype, x.data_ptr(), _ptr(res), gamma.data_ptr(), eps,
           None if res is None else h.data_ptr(), rstd.data_ptr(), y.codes.data_ptr(), y.scales.data_ptr(),
-          _ptr(h8 and h8.codes), _ptr(h8 and h8.scales), rows, cols, _stream(x))
+          _ptr(h8 and h8.codes), _ptr(h8 and h8.scales), rows, cols, _stream(x.device))
     return h, y, rstd, h8
 
 
@@ -198,7 +207,7 @@ def rms_norm_bwd(dy, kept, rstd, gamma, dres=None):
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
     _call("slim_q8_rms_norm_bwd", dy.dtype, dy.data_ptr(), _ptr(h), _ptr(hc), _ptr(hs), rstd.data_ptr(),
           gamma.data_ptr(), _ptr(dres), dh.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), nbytes, rows, cols,
-          _stream(dy))
+          _stream(dy.device))
     return dh, dgamma
 
 
@@ -210,7 +219,7 @@ def gelu(z, checkpoint=True):
     a = empty(rows, cols, device=z.device)
     z8 = empty(rows, cols, device=z.device) if checkpoint else None
     _call("slim_q8_gelu", z.dtype, z.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), _ptr(z8 and z8.codes),
-          _ptr(z8 and z8.scales), rows, cols, _stream(z))
+          _ptr(z8 and z8.scales), rows, cols, _stream(z.device))
     return a, z8
 
 
@@ -223,7 +232,7 @@ def gelu_bwd(da, z8, quantized=False):
     dz = torch.empty_like(da)
     dz8 = empty(rows, cols, device=da.device) if quantized else None
     _call("slim_q8_gelu_bwd", da.dtype, da.data_ptr(), z8.codes.data_ptr(), z8.scales.data_ptr(), dz.data_ptr(),
-          _ptr(dz8 and dz8.codes), _ptr(dz8 and dz8.scales), rows, cols, _stream(da))
+          _ptr(dz8 and dz8.codes), _ptr(dz8 and dz8.scales), rows, cols, _stream(da.device))
     return (dz, dz8) if quantized else dz
 
 
@@ -234,11 +243,11 @@ def matmul(a, w, dtype=torch.bfloat16, out=None):
     _mat(w, "w", BLOCK, None, a.cols, a.codes.device)
     if out is None:
         out = torch.empty((a.rows, w.rows), dtype=dtype, device=a.codes.device)
-    _rows(out, "out")
-    if out.shape != (a.rows, w.rows) or out.device != a.codes.device:
+    elif out.shape != (a.rows, w.rows) or out.device != a.codes.device:
         raise ValueError("out must be [rows, n] on a's device")
+    _rows(out, "out")
     _call("slim_q8_matmul", out.dtype, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(),
-          w.scales.data_ptr(), out.data_ptr(), a.rows, w.rows, a.cols, _stream(out))
+          w.scales.data_ptr(), out.data_ptr(), a.rows, w.rows, a.cols, _stream(out.device))
     return out
 
 
@@ -258,7 +267,8 @@ def wgrad(dy, x, dw=None, accumulate=False):
         raise ValueError("dw must be a contiguous fp32 [n, k] tensor on dy's device")
     nbytes = _lib.slim_q8_wgrad_workspace_bytes(rows, n, x.cols)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
-    binding._check(_lib.slim_q8_wgrad(dy.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(), dw.data_ptr(),
-                                      1 if accumulate else 0, ws.data_ptr(), nbytes, rows, n, x.cols, _stream(dy)),
-                   "slim_q8_wgrad")
+    code = _lib.slim_q8_wgrad(dy.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(), dw.data_ptr(),
+                              1 if accumulate else 0, ws.data_ptr(), nbytes, rows, n, x.cols, _stream(dy.device))
+    if code:
+        raise binding.SlimError(code, "slim_q8_wgrad")
     return dw
