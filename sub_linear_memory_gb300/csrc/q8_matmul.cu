@@ -17,13 +17,16 @@ namespace slim {
 namespace q8 {
 namespace {
 
-// ---- few output tiles: weights as the MMA's M side, k split over a cluster ------
+// ---- few rows: weights as the MMA's M side, k split over a cluster ----------------
 //
-// A tile is 128 weight rows x up to 128 rows of a.  The accumulator's lanes
-// are weight rows, so a warp writes 32 neighbouring columns of out, and the
-// MMA's N is only as wide as the rows of a (16 for one token).  The CTAs of a
-// cluster take a share of k each and add their partial tiles in the order of
-// their ranks through distributed shared memory.
+// A tile is 128 weight rows x all rows of a, up to 128.  The accumulator's
+// lanes are weight rows, so a warp writes neighbouring columns of out, and the
+// MMA's N is only as wide as the rows of a (16 for one token).  What bounds it
+// is latency: the CTAs of a cluster take a share of k each, so that the weight
+// comes through as many SMs as there are, and add their partial tiles in the
+// order of their ranks through distributed shared memory.  In a graph, one
+// token: 4.5 us for 1024 x 4096 (12.3 with k in one piece), 4.0 for 4096 x
+// 1024; 128 tokens: 8.9 (19.6) and 8.2 (11.6).
 namespace sm {
 
 constexpr int kThreads = 256, kStages = 4, kMaxQuads = 48;
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + S_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n0 = blockIdx.y * kBlock, m0 = blockIdx.z * kBlock;
+  const int n0 = blockIdx.y * kBlock;
   const int k0 = (int)((long long)kb * rank / split), k1 = (int)((long long)kb * (rank + 1) / split), nk = k1 - k0;
   const int quads = (nk + 3) / 4;
   if (tid == 0) {
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kThreads)
       if (i >= kStages && !wait(S_EMPTY + s, (i / kStages - 1) & 1)) break;
       mbar_arrive_expect_tx(bar + S_FULL + s, kW + (uint32_t)nt * kBlock);
       tma_load_2d(sbase + s * sb, &mw, bar + S_FULL + s, (k0 + i) * kBlock, n0);
-      tma_load_2d(sbase + s * sb + kW, &ma, bar + S_FULL + s, (k0 + i) * kBlock, m0);
+      tma_load_2d(sbase + s * sb + kW, &ma, bar + S_FULL + s, (k0 + i) * kBlock, 0);
     }
     for (int j = max(0, i - kStages); j < i; ++j) mbar_drain(bar + S_FULL + j % kStages, (j / kStages) & 1);
   } else if (warp == 1 && lane == 0) {
@@ -122,8 +125,8 @@ __global__ void __launch_bounds__(kThreads)
         w |= (kk < nk ? (uint32_t)__ldg(bs + kk) : 127u) << (8 * j);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int m = m0 + 32 * g + lane;
-          const bool on = kk < nk && m < rows && 32 * g < nt;
+          const int m = 32 * g + lane;
+          const bool on = kk < nk && m < rows;
           a[g] |= (on ? (uint32_t)__ldg(a_scales + (size_t)m * pitch + k0 + kk) : 127u) << (8 * j);
         }
       }
@@ -138,17 +141,16 @@ __global__ void __launch_bounds__(kThreads)
     const bool full = wait(S_DONE, 0);
     tc_fence_after();
     const int nn = n0 + 32 * (warp & 3) + lane;
-    const int cols = min(nt, rows - m0);
     if (full) {
-      for (int c = 0; c < cols; c += 16) {
+      for (int c = 0; c < rows; c += 16) {
         float v[16];
         tmem_ld16(tmem_addr(tbase, lanes, c), v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (split > 1) {
             part[(c + i) * kBlock + 32 * (warp & 3) + lane] = v[i];
-          } else if (c + i < cols && nn < n) {
-            const size_t at = (size_t)(m0 + c + i) * n + nn;
+          } else if (c + i < rows && nn < n) {
+            const size_t at = (size_t)(c + i) * n + nn;
             if (F32) static_cast<float *>(out)[at] = v[i];
             else static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v[i]);
           }
@@ -163,10 +165,10 @@ __global__ void __launch_bounds__(kThreads)
     // group of 8 rows.  All loads of a group are under way together: they cross
     // the SMs, and one after the other took most of the kernel (12.3 us for 128
     // rows x 4096 x 1024).
-    const int cols = min(nt, rows - m0), nl = 4 * lane, left = n - n0 - nl;
+    const int nl = 4 * lane, left = n - n0 - nl;
     const uint32_t mine = smem_u32(part);
     if (!*abort_flag && left > 0) {
-      for (int c = 8 * rank + warp; c < cols; c += 8 * split) {
+      for (int c = 8 * rank + warp; c < rows; c += 8 * split) {
         float v[8][4];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[0][e] += v[r][e];
           }
-        const size_t at = (size_t)(m0 + c) * n + n0 + nl;
+        const size_t at = (size_t)c * n + n0 + nl;
         if (F32) {
           float *to = static_cast<float *>(out) + at;
           if (wide) {
@@ -209,11 +211,10 @@ __global__ void __launch_bounds__(kThreads)
 template <bool F32>
 cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                    int rows, int n, int k, int *status, cudaStream_t st) {
-  const int kb = blocks_of(k), tiles_n = blocks_of(n), tiles_m = blocks_of(rows);
-  const int nt = rows >= kBlock ? kBlock : (rows + 15) / 16 * 16;
+  const int kb = blocks_of(k), tiles_n = blocks_of(n), nt = (rows + 15) / 16 * 16;
   // k is split until the SMs have a CTA each, two blocks or more to a CTA
   int split = 1;
-  while (split < 8 && 2 * split * (long long)tiles_n * tiles_m <= 152 && 4 * split <= kb) split *= 2;
+  while (split < 8 && 2 * split * (long long)tiles_n <= 152 && 4 * split <= kb) split *= 2;
   while (split < 8 && (kb + split - 1) / split > 4 * kMaxQuads - 4) split *= 2;
   CUtensorMap mw, ma;
   const uint64_t kp = (uint64_t)kb * kBlock;
@@ -227,7 +228,7 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kBlock, true));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(split, tiles_n, tiles_m);
+  cfg.gridDim = dim3(split, tiles_n);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -539,11 +540,13 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
 
 cudaError_t matmul(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                    bool f32, int rows, int n, int k, int *status, cudaStream_t st) {
-  const long long tiles = (long long)((rows + 255) / 256) * ((n + 255) / 256);
-  if (tiles >= 38) {
+  // Few rows go to the split kernel, with 128 of them 8.9 us for 1024 x 4096
+  // against 13.3 with whole tiles.  Where k is short there is little to split:
+  // 128 rows x 4096 x 1024 8.2 against 7.2 (64 rows 5.9), 512 rows 12.2 against
+  // 7.3 when the split kernel took more rows.
+  if (rows > kBlock || (rows > kBlock / 2 && k <= 1024))
     return f32 ? lg::launch<256, true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
                : lg::launch<256, false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
-  }
   return f32 ? sm::launch<true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
              : sm::launch<false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
 }
