@@ -1,0 +1,124 @@
+"""The 8-bit operators together, as a Performer layer: training and serving
+against the same layer in fp64 without 8-bit rows.
+
+An e4m3 rounding moves a value by up to 2^-4, evenly spread within a binade:
+a relative rms of about 2^-4 / sqrt(3) * 0.7 = 2.6%.  It is random from element
+to element, so a product of two rounded operands is off by sqrt(2) * 2.6% of
+its rms, and a chain of n roundings by sqrt(n) * 2.6%: at most 6 on the way
+forward (6.4%), 12 on the way back to a gradient (9%).  The bars are twice
+that; a wrong term is off by its own size.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lm
+from sub_linear_memory_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+
+B, L, HEADS, D, FF = 2, 200, 4, 64, 512
+DM = HEADS * D
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+
+
+def draw(shape, slot, scale=1.0, dtype=torch.float32):
+    return inputs.gaussian(shape, 7300, slot, scale=scale, dtype=dtype)
+
+
+def weights(favor):
+    from sub_linear_memory_gb300 import binding
+
+    w = {"wqkv": draw((3 * DM, DM), 1, DM ** -0.5), "wo": draw((DM, DM), 2, DM ** -0.5),
+         "w1": draw((FF, DM), 3, DM ** -0.5), "w2": draw((DM, FF), 4, FF ** -0.5),
+         "g1": 1 + 0.1 * draw((DM,), 5), "g2": 1 + 0.1 * draw((DM,), 6)}
+    if favor:  # q and k of unit norm growth would overflow exp: scale them as the inputs are
+        w["wqkv"][: 2 * DM] *= D ** -0.25
+    fw = binding.draw_orf(1, D, 64, seed=3)[0] if favor else None
+    return w, fw
+
+
+def reference(w, fw, x, r, dh, df):
+    """The layer in fp64 by autograd."""
+    t = {k: v.double().requires_grad_(True) for k, v in w.items()}
+    x = x.double().requires_grad_(True)
+    norm = lambda h, g: h / torch.sqrt((h * h).mean(-1, keepdim=True) + 1e-5) * g
+    h = x + r.double()
+    qkv = (norm(h, t["g1"]) @ t["wqkv"].t()).view(B, L, 3, HEADS, D).permute(2, 0, 3, 1, 4)
+    o = lm.linear_attention(qkv[0], qkv[1], qkv[2], None if fw is None else fw.double().cpu())
+    h2 = h + o.transpose(1, 2).reshape(B * L, DM) @ t["wo"].t()
+    f = lm.gelu(norm(h2, t["g2"]) @ t["w1"].t()) @ t["w2"].t()
+    ((h2 * dh.double()).sum() + (f * df.double()).sum()).backward()
+    return h2.detach(), f.detach(), x.grad, {k: v.grad for k, v in t.items()}
+
+
+def rel(got, want):
+    got, want = got.detach().double().cpu(), want.double()
+    return float((got - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("favor", [True, False])
+def test_training_step(favor):
+    from sub_linear_memory_gb300 import binding
+    from sub_linear_memory_gb300.layer8 import Layer8
+
+    w, fw = weights(favor)
+    bf = lambda shape, slot, scale=1.0: draw(shape, slot, scale, torch.bfloat16)
+    x, r = bf((B * L, DM), 10), bf((B * L, DM), 11, 0.5)
+    dh, df = bf((B * L, DM), 12, 1e-3), bf((B * L, DM), 13, 1e-3)
+    layer = Layer8(HEADS, fw, **{k: v.cuda() for k, v in w.items()}, chunk=64)
+    (h2, f), kept = layer.forward(x.cuda(), r.cuda(), B)
+    dx, grads = layer.backward(dh.cuda(), df.cuda(), kept)
+    binding.sync_status()
+    h2_ref, f_ref, dx_ref, grads_ref = reference(w, fw, x, r, dh, df)
+    assert rel(h2, h2_ref) <= 0.13 and rel(f, f_ref) <= 0.13
+    assert rel(dx, dx_ref) <= 0.18
+    for name, want in grads_ref.items():
+        assert rel(grads[name], want) <= 0.18, name
+    assert sum(t.codes.element_size() * t.codes.numel() for t in kept if hasattr(t, "codes")) == B * L * (5 * DM + 2 * FF)
+
+
+@pytest.mark.parametrize("favor", [True, False])
+def test_serving(favor):
+    """Prefill and one-token steps give the forward's rows: the same roundings,
+    but for sums in another order (a code may fall on the other side of a
+    border, one step of 2^-3 in some of the terms)."""
+    from sub_linear_memory_gb300 import binding
+    from sub_linear_memory_gb300.layer8 import Layer8
+
+    w, fw = weights(favor)
+    x, r = draw((B, L, DM), 20, 1.0, torch.bfloat16).cuda(), draw((B, L, DM), 21, 0.5, torch.bfloat16).cuda()
+    layer = Layer8(HEADS, fw, **{k: v.cuda() for k, v in w.items()}, chunk=64)
+    rows = lambda t, n: t[:, :n].reshape(B * n, DM).contiguous()
+    (h2, f), _ = layer.forward(rows(x, L), rows(r, L), B)
+    n = L - 3
+    (h2p, fp), state = layer.prefill(rows(x, n), rows(r, n), B)
+    for got, want in ((h2p, h2), (fp, f)):
+        assert rel(got, want.view(B, L, DM)[:, :n].reshape(B * n, DM).cpu()) <= 0.05
+    for i in range(n, L):
+        h2d, fd = layer.decode(x[:, i].contiguous(), r[:, i].contiguous(), state)
+        binding.sync_status()
+        assert rel(h2d, h2.view(B, L, DM)[:, i].cpu()) <= 0.05
+        assert rel(fd, f.view(B, L, DM)[:, i].cpu()) <= 0.05
+    # the first norm of a model has nothing to add
+    (h2, _), _ = layer.forward(rows(x, L), None, B)
+    assert torch.isfinite(h2.float()).all()
+
+
+def test_new_weights():
+    from sub_linear_memory_gb300.layer8 import Layer8
+
+    w, _ = weights(False)
+    layer = Layer8(HEADS, None, **{k: v.cuda() for k, v in w.items()}, chunk=64)
+    x = draw((B * L, DM), 30, 1.0, torch.bfloat16).cuda()
+    (_, f), _ = layer.forward(x, None, B)
+    layer.load(w2=-w["w2"].cuda())
+    (_, g), _ = layer.forward(x, None, B)
+    assert torch.equal(f, -g)
+    with pytest.raises(ValueError):
+        layer.load(g1=w["g1"].cuda())
