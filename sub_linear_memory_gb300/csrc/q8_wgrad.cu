@@ -3,7 +3,7 @@
 //
 // The sum runs over rows, across which the scales of x differ, so the tensor
 // cores cannot apply them; but code * 2^e is exactly a bf16 number, and dy is
-// bf16.  Four warps turn each tile of codes into bf16 in shared memory (shifts,
+// bf16.  Eight warps turn each tile of codes into bf16 in shared memory (shifts,
 // masks and a packed multiply) while the tensor cores (kind::f16, both operands
 // MN-major) work on the tiles before.
 //
@@ -16,8 +16,8 @@
 // Rounding: the tensor cores add into their fp32 accumulator with truncation;
 // over the 4096 additions of 65536 rows that lost 4e-5 of the result.  The
 // accumulator is therefore emptied every 20 steps (80 additions) into
-// registers of eight other warps, which add with rounding to nearest, while
-// the MMAs go on in a second accumulator.
+// registers of the eight warps, which add with rounding to nearest, while the
+// MMAs go on in a second accumulator.
 //
 // Split: the rows are cut into steps of 64.  While there are as many tiles as
 // pairs, a pair takes a whole tile.  The remaining tiles, fewer than the pairs,
@@ -43,7 +43,7 @@ constexpr int kPairs = 76;      // one CTA for each of 152 SMs
 constexpr int kTn = 256, kTk = 256, kStep = 64;  // a pair's tile and rows of a step
 constexpr int kMinSteps = 8;    // per pair: a partial tile costs about this much
 constexpr int kWindow = 20;     // steps in one accumulator
-constexpr int kThreads = 512;   // loads, MMA, scales; four converting, eight adding warps
+constexpr int kThreads = 384;   // codes, MMA, dy, scales; eight warps that convert and add
 // Two rings: dy with the converted tiles (freed together by the MMAs), and the
 // codes (freed by the converting warps).
 constexpr int kBufs = 5, kCodes = 6;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar + S_ACC + b, 1);
-      mbar_init(bar + S_ACCFREE + b, 16);  // adding warps of both CTAs
+      mbar_init(bar + S_ACCFREE + b, 16);  // the eight warps of both CTAs
     }
     mbar_init(bar + S_DONE, 1);
     *abort_flag = 0;
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive_pair(map_peer(smem_u32(bar + b), 0));
   };
-  // Registers of the launch: 512 x 128.  The warpgroups' shares (64 + 96 + 2 x
-  // 176, times 128) come to these 65536.
+  // Registers of the launch: 384 x 168.  The warpgroups' shares (64 + 2 x 216,
+  // times 128) come to 63488 of these 64512.
   if (warp < 4) {
     regs_dec<64>();
     if (warp == 0 && lane == 0) {
@@ -319,89 +319,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       copy_async_wait();
     }
-  } else if (warp < 8) {
-    regs_dec<96>();
-    // Two warps convert a step, the other two the next: what a step costs
-    // besides its arithmetic (waits, the proxy fence, arrivals) overlaps.
-    // Thread: 16 codes of rows row0 + 8 j.
-    const int chunk = lane & 7, row0 = 4 * (warp & 1) + (lane >> 3);
+  } else {
+    regs_inc<216>();
+    // Two warps convert a step, the next two the next: what a step costs besides
+    // its arithmetic (waits, the proxy fence, arrivals) overlaps.  The same
+    // warps empty the accumulators, since adding takes them 3% of the time; with
+    // four warps for one and eight for the other a step took 990 cycles.
+    // Converting, a thread has 16 codes of rows row0 + 8 j.
+    const int mate = (warp >> 1) & 3, chunk = lane & 7, row0 = 4 * (warp & 1) + (lane >> 3);
     // A thread's two 8-byte loads and two 16-byte stores of a row, in an order
     // that keeps the lanes served together on distinct banks: half of them
     // begin with the second half.
     const bool swap = ((chunk >> 2) ^ (lane >> 3)) & 1;
-    Walk p(cut, pair, rank);
-    for (int i = 0; p.more && ok; p.next(), ++i) {
-      if ((i & 1) != ((warp >> 1) & 1)) continue;
-      const int s = i % kCodes, b = i % kBufs;
-      if (i >= kBufs && !wait_warp(S_FREE + b, (uint32_t)(i / kBufs - 1) & 1)) break;
-      if (!TMA_DY) {  // rows that TMA cannot step over: loaded here into the same layout
-        const int r0 = p.step * kStep;
-        for (int x = 32 * (warp & 1) + lane; x < kStep * kBlock; x += 64) {
-          const int r = x / kBlock, c = x % kBlock;
-          const __nv_bfloat16 v =
-              r0 + r < rows && p.n0 + c < n ? dy[(size_t)(r0 + r) * n + p.n0 + c] : __float2bfloat16_rn(0.f);
-          *reinterpret_cast<__nv_bfloat16 *>(smem + b * kDBytes + sw128_offset(r, c, kStep)) = v;
-        }
-      }
-      if (!wait_warp(S_CODES + s, (uint32_t)(i / kCodes) & 1)) break;
-      const uint32_t from = sbase + oCodes + s * kCBytes + chunk * 16, to = sbase + oB + b * kBBytes;
-      // Everything that waits for memory or for other lanes comes before the
-      // arithmetic: between the stores, which keep their order, each shuffle
-      // and load would wait for its turn.
-      uint32_t x[kStep / 8][4], f[kStep / 8];
-#pragma unroll
-      for (int j = 0; j < kStep / 8; ++j) {
-        const uint32_t at = from + (row0 + 8 * j) * kBlock;
-        ld_shared_v2(at ^ (swap ? 8u : 0u), x[j][0], x[j][1]);
-        ld_shared_v2(at ^ (swap ? 0u : 8u), x[j][2], x[j][3]);
-      }
-      // factor of one row a lane (row 4 (warp & 1) + lane % 4 + 8 (lane / 4))
-      const int mine = 4 * (warp & 1) + (lane & 3) + 8 * (lane >> 2);
-      int byte = 127;
-      if (p.step * kStep + mine < rows && p.blk * kBlock < k)
-        byte = smem[oTable + s * kTable + mine * 4 + (p.blk & 3)];
-      uint32_t second;
-      const uint32_t first = factor(byte, second);
-      const bool twice = __any_sync(0xffffffffu, second != 0);
-      if (second == 0) second = 0x3f803f80u;  // one, for the rows that need none
-#pragma unroll
-      for (int j = 0; j < kStep / 8; ++j) f[j] = __shfl_sync(0xffffffffu, first, 4 * j + (lane >> 3));
-#pragma unroll
-      for (int j = 0; j < kStep / 8; ++j) {
-        const int r = row0 + 8 * j;
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          widen4(x[j][e], o[2 * e], o[2 * e + 1]);
-          o[2 * e] = mul_bf16x2(o[2 * e], f[j]);
-          o[2 * e + 1] = mul_bf16x2(o[2 * e + 1], f[j]);
-        }
-        if (twice) {
-          const uint32_t g = __shfl_sync(0xffffffffu, second, 4 * j + (lane >> 3));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], g);
-        }
-        const uint32_t at = to + sw128_offset(r, 16 * chunk, kStep) ^ (swap ? 16u : 0u);
-        st_shared_v4(at, o[0], o[1], o[2], o[3]);
-        st_shared_v4(at ^ 16u, o[4], o[5], o[6], o[7]);
-      }
-      fence_async_smem();
-      arrive_leader(S_BFULL + b);
-      arrive(S_CODESFREE + s);
-    }
-  } else {
-    regs_inc<176>();
-    // this thread's row of the tile (a TMEM lane), 128 of its 256 columns
+    // Adding, it has a row of the tile (a TMEM lane), and 128 of its 256 columns.
     const uint32_t lanes = 32u * (warp & 3);
-    const int c0 = warp < 12 ? 0 : 128, nr = rank * kBlock + (int)lanes + lane;
-    int win = 0;
+    const int c0 = warp < 8 ? 0 : 128, nr = rank * kBlock + (int)lanes + lane;
+    int i = 0, win = 0;
     Seg seg;
     for (int x = 0; ok && cut.get(pair, x, seg); ++x) {
       const bool whole = seg.slot < 0;
+      const int n0 = seg.tile / cut.tiles_k * kTn, blk = seg.tile % cut.tiles_k * 2 + rank;
       float sum[128];
 #pragma unroll
       for (int e = 0; e < 128; ++e) sum[e] = 0.f;
-      for (int first = seg.s0; first < seg.s1 && ok; first += kWindow, ++win) {
+      // the next accumulator that is done, into the sums
+      auto take = [&] {
         wait_warp(S_ACC + (win & 1), (uint32_t)(win >> 1) & 1);
         tc_fence_after();
 #pragma unroll
@@ -413,7 +355,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         arrive_leader(S_ACCFREE + (win & 1));
+        ++win;
+      };
+      int done = seg.s0 + kWindow;  // the end of the next accumulator to add
+      for (int step = seg.s0; step < seg.s1 && ok; ++step, ++i) {
+        // kBufs steps on, a step's buffer is free only when the first step of the
+        // accumulator after it has been multiplied: no waiting here
+        if (step == done + kBufs) {
+          take();
+          done += kWindow;
+        }
+        if ((i & 3) != mate) continue;
+        const int s = i % kCodes, b = i % kBufs, r0 = step * kStep;
+        if (i >= kBufs && !wait_warp(S_FREE + b, (uint32_t)(i / kBufs - 1) & 1)) break;
+        if (!TMA_DY) {  // rows that TMA cannot step over: loaded here into the same layout
+          const int nn = n0 + rank * kBlock;
+          for (int y = 32 * (warp & 1) + lane; y < kStep * kBlock; y += 64) {
+            const int r = y / kBlock, c = y % kBlock;
+            const __nv_bfloat16 v =
+                r0 + r < rows && nn + c < n ? dy[(size_t)(r0 + r) * n + nn + c] : __float2bfloat16_rn(0.f);
+            *reinterpret_cast<__nv_bfloat16 *>(smem + b * kDBytes + sw128_offset(r, c, kStep)) = v;
+          }
+        }
+        if (!wait_warp(S_CODES + s, (uint32_t)(i / kCodes) & 1)) break;
+        const uint32_t from = sbase + oCodes + s * kCBytes + chunk * 16, to = sbase + oB + b * kBBytes;
+        // Everything that waits for memory or for other lanes comes before the
+        // arithmetic: between the stores, which keep their order, each shuffle
+        // and load would wait for its turn.
+        uint32_t w[kStep / 8][4], f[kStep / 8];
+#pragma unroll
+        for (int j = 0; j < kStep / 8; ++j) {
+          const uint32_t at = from + (row0 + 8 * j) * kBlock;
+          ld_shared_v2(at ^ (swap ? 8u : 0u), w[j][0], w[j][1]);
+          ld_shared_v2(at ^ (swap ? 0u : 8u), w[j][2], w[j][3]);
+        }
+        // factor of one row a lane (row 4 (warp & 1) + lane % 4 + 8 (lane / 4))
+        const int mine = 4 * (warp & 1) + (lane & 3) + 8 * (lane >> 2);
+        int byte = 127;
+        if (r0 + mine < rows && blk * kBlock < k) byte = smem[oTable + s * kTable + mine * 4 + (blk & 3)];
+        uint32_t second;
+        const uint32_t first = factor(byte, second);
+        const bool twice = __any_sync(0xffffffffu, second != 0);
+        if (second == 0) second = 0x3f803f80u;  // one, for the rows that need none
+        arrive(S_CODESFREE + s);                // all of the step's codes and scales are in registers
+#pragma unroll
+        for (int j = 0; j < kStep / 8; ++j) f[j] = __shfl_sync(0xffffffffu, first, 4 * j + (lane >> 3));
+#pragma unroll
+        for (int j = 0; j < kStep / 8; ++j) {
+          const int r = row0 + 8 * j;
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            widen4(w[j][e], o[2 * e], o[2 * e + 1]);
+            o[2 * e] = mul_bf16x2(o[2 * e], f[j]);
+            o[2 * e + 1] = mul_bf16x2(o[2 * e + 1], f[j]);
+          }
+          if (twice) {
+            const uint32_t g = __shfl_sync(0xffffffffu, second, 4 * j + (lane >> 3));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], g);
+          }
+          const uint32_t at = (to + sw128_offset(r, 16 * chunk, kStep)) ^ (swap ? 16u : 0u);
+          st_shared_v4(at, o[0], o[1], o[2], o[3]);
+          st_shared_v4(at ^ 16u, o[4], o[5], o[6], o[7]);
+        }
+        fence_async_smem();
+        arrive_leader(S_BFULL + b);
       }
+      for (; ok && done - kWindow < seg.s1; done += kWindow) take();
       if (!ok) break;
 #pragma unroll
       for (int e = 0; e < 128; e += 4) {  // the columns' own order
@@ -422,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum[e + 2] = u;
       }
       // into dw, or into this pair's partial tile
-      const int n0 = seg.tile / cut.tiles_k * kTn, kk = seg.tile % cut.tiles_k * kTk + c0;
+      const int kk = seg.tile % cut.tiles_k * kTk + c0;
       float *to = whole ? dw + (size_t)(n0 + nr) * k + kk
                         : partial + (size_t)seg.slot * (kTn * kTk) + (size_t)nr * kTk + c0;
       const int left = whole ? (n0 + nr < n ? k - kk : 0) : kTk;
