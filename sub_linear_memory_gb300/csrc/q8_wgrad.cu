@@ -72,6 +72,11 @@ struct Cut {
   int tail, extras;   // and `tail` last steps, shared out over the `extras` left-over pairs
 
   __host__ __device__ long long tail_begin(int e) const { return (long long)rest * tail * e / extras; }
+  // The left-over pair that holds step u of the tails: the last e whose
+  // tail_begin(e) = floor(rest tail e / extras) is not past u.
+  __host__ __device__ int tail_owner(long long u) const {
+    return (int)(((u + 1) * extras - 1) / ((long long)rest * tail));
+  }
   // Segment `i` of a pair; false past its last.
   __host__ __device__ bool get(int pair, int i, Seg &s) const {
     if (i < waves) {
@@ -477,10 +482,11 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float *partial, f
 #pragma unroll 4
   for (int j = 0; j < parts; ++j) add(t * cut.parts + j);
   if (cut.tail) {
-    // the left-over pairs that hold steps of this tile's tail
-    const long long first = (long long)t * cut.tail, last = first + cut.tail;
-    for (int e = 0; e < cut.extras; ++e)
-      if (max(cut.tail_begin(e), first) < min(cut.tail_begin(e + 1), last)) add(cut.parts * cut.rest + t + e);
+    // the left-over pairs that hold steps of this tile's tail (fewer than there
+    // are steps, so none of them is empty)
+    const long long first = (long long)t * cut.tail;
+    const int to = cut.tail_owner(first + cut.tail - 1);
+    for (int e = cut.tail_owner(first); e <= to; ++e) add(cut.parts * cut.rest + t + e);
   }
   const float s[4] = {v.x, v.y, v.z, v.w};
   float *to = dw + (size_t)nn * k + kk;
