@@ -42,6 +42,7 @@ namespace {
 constexpr int kPairs = 76;      // one CTA for each of 152 SMs
 constexpr int kTn = 256, kTk = 256, kStep = 64;  // a pair's tile and rows of a step
 constexpr int kMinSteps = 8;    // per pair: a partial tile costs about this much
+constexpr int kSegSteps = 16;   // a part's own cost, in steps (65536 x 1024 x 4096: 5.5 us)
 constexpr int kWindow = 20;     // steps in one accumulator
 constexpr int kThreads = 384;   // codes, MMA, dy, scales; eight warps that convert and add
 // Two rings: dy with the converted tiles (freed together by the MMAs), and the
@@ -110,8 +111,11 @@ Cut cut_of(int rows, int n, int k) {
   c.parts = c.part = c.tail = c.extras = 0;
   if (c.rest) {
     c.parts = c.pairs / c.rest;
-    c.part = (int)(((long long)c.steps * c.rest + c.pairs - 1) / c.pairs);
     c.extras = c.pairs - c.parts * c.rest;
+    // a left-over pair has parts of several tiles, each of which costs it
+    // kSegSteps steps' time to empty and write
+    c.part = c.extras ? (int)std::min<long long>(c.steps, ((long long)c.rest * (c.steps + kSegSteps) + c.pairs - 1) / c.pairs)
+                      : (c.steps + c.parts - 1) / c.parts;
     c.tail = c.extras ? std::max(0, c.steps - c.parts * c.part) : 0;
   }
   return c;
@@ -435,29 +439,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum[e + 1] = sum[e + 2];
         sum[e + 2] = u;
       }
-      // into dw, or into this pair's partial tile
-      const int kk = seg.tile % cut.tiles_k * kTk + c0;
-      float *to = whole ? dw + (size_t)(n0 + nr) * k + kk
-                        : partial + (size_t)seg.slot * (kTn * kTk) + (size_t)nr * kTk + c0;
-      const int left = whole ? (n0 + nr < n ? k - kk : 0) : kTk;
-      const bool add = whole && accumulate;
-      if (!whole || wide) {
+      if (!whole) {
+        // a partial tile is [64 groups of 4 columns][256 rows][4]: a warp's
+        // stores are whole lines
+        float4 *to = reinterpret_cast<float4 *>(partial + (size_t)seg.slot * (kTn * kTk)) + c0 / 4 * kTn + nr;
+#pragma unroll
+        for (int e = 0; e < 128; e += 4) to[e / 4 * kTn] = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+        continue;
+      }
+      const int kk = seg.tile % cut.tiles_k * kTk + c0, left = n0 + nr < n ? k - kk : 0;
+      float *to = dw + (size_t)(n0 + nr) * k + kk;
+      if (wide) {
 #pragma unroll
         for (int e = 0; e < 128; e += 4) {
           if (e < left) {
             float4 *p = reinterpret_cast<float4 *>(to + e);
-            float4 x = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-            if (add) {
+            float4 v = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+            if (accumulate) {
               const float4 o = *p;
-              x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
+              v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
             }
-            *p = x;
+            *p = v;
           }
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 128; ++e)
-          if (e < left) to[e] = add ? to[e] + sum[e] : sum[e];
+          if (e < left) to[e] = accumulate ? to[e] + sum[e] : sum[e];
       }
     }
   }
@@ -466,16 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc_pair(tbase, 512);
 }
 
-// dw of the tiles that are cut along the rows, four columns a thread.
+// dw of the tiles that are cut along the rows: 32 rows x 32 columns a CTA, read
+// as the partial tiles lie (four columns a thread, a warp along the rows) and
+// turned in shared memory, so that loads and stores are whole lines.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const float *partial, float *dw, Cut cut, int accumulate, int n,
                                                          int k) {
+  __shared__ float turned[32][36];
   const int t = blockIdx.x, tile = cut.waves * cut.pairs + t;
-  const int at = (int)blockIdx.y * 1024 + threadIdx.x * 4, r = at / kTk, c = at % kTk;
-  const int nn = tile / cut.tiles_k * kTn + r, kk = tile % cut.tiles_k * kTk + c;
-  if (nn >= n || kk >= k) return;
+  const int r0 = (int)blockIdx.y % 8 * 32, q0 = (int)blockIdx.y / 8 * 8;  // first row, first group of four columns
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const float4 *from = reinterpret_cast<const float4 *>(partial) + (size_t)(q0 + q) * kTn + r0 + lane;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](int slot) {
-    const float4 x = *reinterpret_cast<const float4 *>(partial + (size_t)slot * (kTn * kTk) + at);
+    const float4 x = from[(size_t)slot * (kTn * kTk / 4)];
     v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
   };
   const int parts = min(cut.parts, (cut.steps + cut.part - 1) / cut.part);
@@ -488,11 +499,15 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float *partial, f
     const int to = cut.tail_owner(first + cut.tail - 1);
     for (int e = cut.tail_owner(first); e <= to; ++e) add(cut.parts * cut.rest + t + e);
   }
-  const float s[4] = {v.x, v.y, v.z, v.w};
+  *reinterpret_cast<float4 *>(&turned[lane][4 * q]) = v;
+  __syncthreads();
+  const int r = threadIdx.x >> 3, c = threadIdx.x % 8 * 4;
+  const int nn = tile / cut.tiles_k * kTn + r0 + r, kk = tile % cut.tiles_k * kTk + 4 * q0 + c;
+  if (nn >= n) return;
   float *to = dw + (size_t)nn * k + kk;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (kk + e < k) to[e] = accumulate ? to[e] + s[e] : s[e];
+    if (kk + e < k) to[e] = accumulate ? to[e] + turned[r][c + e] : turned[r][c + e];
 }
 
 }  // namespace
