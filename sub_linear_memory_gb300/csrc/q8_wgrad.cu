@@ -41,8 +41,8 @@ namespace {
 
 constexpr int kPairs = 76;      // one CTA for each of 152 SMs
 constexpr int kTn = 256, kTk = 256, kStep = 64;  // a pair's tile and rows of a step
-constexpr int kMinSteps = 8;    // per pair: a partial tile costs about this much
-constexpr int kSegSteps = 16;   // a part's own cost, in steps (65536 x 1024 x 4096: 5.5 us)
+constexpr int kMinSteps = 4;    // per pair: about what writing and joining a partial tile costs
+constexpr int kSegSteps = 8;    // a part's own cost, in steps (381 us with 16, 377 with 8, 381 with 24)
 constexpr int kWindow = 20;     // steps in one accumulator
 constexpr int kThreads = 384;   // codes, MMA, dy, scales; eight warps that convert and add
 // Two rings: dy with the converted tiles (freed together by the MMAs), and the
