@@ -419,6 +419,7 @@ slim_status slim_q8_gelu_bwd_f32(const float *da, const void *z_codes, const voi
  * (R = 128).  Products and sums in fp32 on the tensor cores (tcgen05, scales
  * applied per 128 columns), rounded once to out.  Rows past `rows` and columns
  * past n of the buffers are never read or written.  k = 0 gives zeros.
+ * k <= 131072, rows and n <= 8388480, else SLIM_ERR_UNSUPPORTED.
  * Data gradient: a = 8 bits of dY, b = the transposed packed weight. */
 slim_status slim_q8_matmul(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales,
                            void *out, int rows, int n, int k, slim_stream_t stream);
@@ -429,7 +430,7 @@ slim_status slim_q8_matmul_f32(const void *a_codes, const void *a_scales, const 
  * dw [n][k] (fp32) = sum over rows of dy[row][n] * x[row][k], added to dw
  * where accumulate is not 0.  dy: bf16 [rows][n]; x: R = 1.  Products of the
  * bf16 dy and the (exactly bf16) values of x, summed in fp32 in an order that
- * depends on the shape and the device's SM count alone.  workspace: 16-byte
+ * depends on the shape alone.  workspace: 16-byte
  * aligned device memory of slim_q8_wgrad_workspace_bytes(rows, n, k) bytes
  * (NULL where that is 0). */
 slim_status slim_q8_wgrad(const void *dy, const void *x_codes, const void *x_scales, float *dw, int accumulate,

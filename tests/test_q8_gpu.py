@@ -304,7 +304,8 @@ def test_matmul(q8, rows, n, k, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows, n, k", [(2560, 1024, 1024), (9728, 256, 128), (2433, 1033, 700), (1300, 2056, 392),
                                         (5000, 520, 1928), (257, 9999, 264), (12000, 1001, 136), (3000, 1536, 4000),
-                                        (20001, 1033, 520), (40000, 640, 1160)])
+                                        (20001, 1033, 520), (40000, 640, 1160), (300, 8, 256), (300, 24, 1500),
+                                        (129, 1, 40), (66, 100, 1024), (128, 4099, 1000)])
 def test_matmul_many_tiles(q8, rows, n, k, dtype):
     a, w = pair(q8, rows, n, k, 2)
     out = check_matmul(q8, a, w, dtype)
@@ -438,3 +439,37 @@ def test_other_stream_and_graph(q8):
     want = step()
     sync()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_offsets_past_32_bits(q8):
+    """Matrices of more than 2^31 elements: the last rows, and an odd width's."""
+    rows, cols = 70001, 32768
+    x = torch.empty((rows, cols), dtype=BF16, device="cuda").uniform_(-3, 3)
+    q = q8.quantize(x)
+    last = np64(x[-2:])
+    codes, scales = ref.quantize(last)
+    assert np.array_equal(np64(q.codes[-2:].float()), codes)
+    assert np.array_equal(q.scales[-2:].cpu().numpy(), scales)
+    x = q8.dequantize(q)
+    sync()
+    assert np.array_equal(np64(x[-2:]), ref.values(codes, scales, cols))
+    dz = q8.gelu_bwd(x, q)
+    sync()
+    held = ref.values(codes, scales, cols)
+    assert np.all(np.abs(np64(dz[-2:]) - held * ref.gelu_slope(held)) <= 2.0 ** -8 * np.abs(held * 1.2) + 1e-5)
+    del x, q, dz
+    rows, n, k = 262200, 8200, 128
+    a = q8.quantize(torch.randn((rows, k), device="cuda"))
+    w = q8.pack_weight(torch.randn((n, k), device="cuda"), transpose=False)[0]
+    out = q8.matmul(a, w)
+    sync()
+    av = ref.values(*stored(q8.Q8(a.codes[-3:], a.scales[-3:], k)), k)
+    want = av @ ref.values(*stored(w), k, 128).T
+    assert np.all(np.abs(np64(out[-3:]) - want) <= 2.0 ** -8 * np.abs(want) + 1e-4)
+    dw = q8.wgrad(out, a)
+    sync()
+    dw64 = torch.zeros((8, k), dtype=torch.float64, device="cuda")
+    values = q8.dequantize(a, F32)
+    for r in range(0, rows, 65536):
+        dw64 += out[r:r + 65536, -8:].double().t() @ values[r:r + 65536].double()
+    assert np.linalg.norm(np64(dw[-8:]) - np64(dw64)) <= 2e-6 * np.linalg.norm(np64(dw64))

@@ -206,3 +206,20 @@ def test_python_checks():
                  lambda: q8.rms_norm_bwd(cpu, bad, cpu[0], cpu[0]), lambda: q8.pack_weight(cpu), lambda: q8.gelu(cpu)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_register_shares_hold_without_spills(tmp_path):
+    """The weight gradient's warpgroups trade registers (setmaxnreg): each role
+    has to fit its share, so the kernel must compile without spills."""
+    import os
+    import shutil
+    import subprocess
+
+    nvcc = os.environ.get("NVCC", "nvcc")
+    if shutil.which(nvcc) is None:
+        pytest.skip("no nvcc")
+    src = os.path.join(build.CSRC, "q8_wgrad.cu")
+    out = subprocess.run([nvcc, *build.ARCH, *build.FLAGS, "-Xptxas", "-v", "-c", src, "-o", str(tmp_path / "w.o")],
+                         capture_output=True, text=True, check=True)
+    spills = [line for line in (out.stdout + out.stderr).splitlines() if "spill stores" in line]
+    assert spills and all("0 bytes spill stores, 0 bytes spill loads" in line for line in spills)
