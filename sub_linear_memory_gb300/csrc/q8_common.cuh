@@ -40,8 +40,8 @@ __device__ __forceinline__ float scale_value(int byte) {
   return __uint_as_float(byte == kScaleNan ? 0x7fffffffu : byte == 0 ? 0x00400000u : (uint32_t)byte << 23);
 }
 
-// Largest magnitude (its bits) of 8 values, two to an instruction, and over
-// the 16 threads of a block.  max.NaN returns a NaN where there is one.
+// Largest magnitude (its bits) of 8 values, two to an instruction.  max.NaN
+// returns a NaN where there is one.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float m;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
@@ -53,10 +53,17 @@ __device__ __forceinline__ uint32_t amax8(const float *v) {
   m = max3_nan(m, fabsf(v[5]), fabsf(v[6]));
   return __float_as_uint(max3_nan(m, fabsf(v[7]), 0.f));
 }
-__device__ __forceinline__ uint32_t amax_block(uint32_t m) {
+
+// The scale bytes of two blocks from this thread's share of each; the blocks'
+// 16 threads agree.  A scale byte never falls as the magnitude grows (a NaN
+// block's is the largest), so the bytes can be compared in place of the
+// magnitudes, and two of them travel in one shuffle.
+__device__ __forceinline__ void block_bytes(uint32_t amax0, uint32_t amax1, int &byte0, int &byte1) {
+  uint32_t m = (uint32_t)scale_byte(amax0) | (uint32_t)scale_byte(amax1) << 16;
 #pragma unroll
-  for (int o = 1; o < kVecs; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  for (int o = 1; o < kVecs; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  byte0 = (int)(m & 0xffffu);
+  byte1 = (int)(m >> 16);
 }
 
 // The codes of a NaN block: NaN in the `left` columns inside the row.
@@ -199,13 +206,11 @@ struct Shape8 {
 };
 __host__ __device__ inline Shape8 shape8(int rows, int cols) { return Shape8{rows, cols, blocks_of(cols), scale_pitch(cols)}; }
 
-// Quantize this thread's 8 values of block `blk` of a row (the block's 16
-// threads call together, every thread of the warp calls) and store the codes
-// and, once, the scale byte; the last block's thread also writes the bytes
-// that pad the row's scales.  live: the block exists.
-__device__ __forceinline__ void put_block8(const float *v, const Mat8 &m, const Shape8 &s, long long row, int blk,
-                                           int lane16, bool live) {
-  const int byte = scale_byte(amax_block(amax8(v)));
+// Store the codes of this thread's 8 values of block `blk` of a row under its
+// scale byte and, once, that byte; the last block's thread also writes the
+// bytes that pad the row's scales.  live: the block exists.
+__device__ __forceinline__ void put8(const float *v, int byte, const Mat8 &m, const Shape8 &s, long long row, int blk,
+                                     int lane16, bool live) {
   const int col = blk * kBlock + lane16 * kVec;
   const uint2 c = encode8(v, byte, s.cols - col);
   if (!live) return;

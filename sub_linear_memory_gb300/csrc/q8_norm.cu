@@ -104,8 +104,7 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
   for (int c = 0; c < NC; ++c) {
     const int chunk = c * 32 * W + l, blk = chunk / kVecs, col = chunk * kVec;
     const bool on = live && blk < s.nb;
-    if (hq.codes) put_block8(v[c], hq, s, row, blk, lane16, on);
-    float g[kVec];
+    float g[kVec], out[kVec];
     load8<float, VEC>(gamma + col, s.cols - col, g);
 #pragma unroll
     for (int i = 0; i < kVec; i += 2) {
@@ -114,10 +113,13 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
       const float2 lost = __ffma2_rn(x, rest2, __ffma2_rn(x, root2, make_float2(-n.x, -n.y)));
       const float2 full = __ffma2_rn(n, gg, __fmul2_rn(lost, gg));
       // columns past the row are 0 whatever root is
-      v[c][i] = (VEC ? col : col + i) < s.cols ? full.x : 0.f;
-      v[c][i + 1] = (VEC ? col : col + i + 1) < s.cols ? full.y : 0.f;
+      out[i] = (VEC ? col : col + i) < s.cols ? full.x : 0.f;
+      out[i + 1] = (VEC ? col : col + i + 1) < s.cols ? full.y : 0.f;
     }
-    put_block8(v[c], y, s, row, blk, lane16, on);
+    int byte_y, byte_h;
+    block_bytes(amax8(out), amax8(v[c]), byte_y, byte_h);
+    put8(out, byte_y, y, s, row, blk, lane16, on);
+    if (hq.codes) put8(v[c], byte_h, hq, s, row, blk, lane16, on);
   }
 }
 

@@ -75,20 +75,31 @@ __global__ void __launch_bounds__(kEltThreads, kEltCtas) quantize_kernel(const T
     const int col = blk[u] * kBlock + lane16 * kVec;
     load8<T, VEC>(x + (size_t)row[u] * s.cols + col, b < blocks ? s.cols - col : 0, v[u]);
   }
+  auto live = [&](int u) { return first + u * (kEltThreads / kVecs) < blocks; };
+  if constexpr (GELU) {
 #pragma unroll
-  for (int u = 0; u < kEltUnroll; ++u) {
-    const bool live = first + u * (kEltThreads / kVecs) < blocks;
-    if (GELU) {
-      if (z.codes) put_block8(v[u], z, s, row[u], blk[u], lane16, live);
+    for (int u = 0; u < kEltUnroll; ++u) {
+      float act[kVec];
 #pragma unroll
       for (int i = 0; i < kVec; i += 2) {
         float2 cdf, pdf;
         normal_parts(make_float2(v[u][i], v[u][i + 1]), cdf, pdf);
-        v[u][i] *= cdf.x;
-        v[u][i + 1] *= cdf.y;
+        act[i] = v[u][i] * cdf.x;
+        act[i + 1] = v[u][i + 1] * cdf.y;
       }
+      int byte_a, byte_z;
+      block_bytes(amax8(act), amax8(v[u]), byte_a, byte_z);
+      put8(act, byte_a, a, s, row[u], blk[u], lane16, live(u));
+      if (z.codes) put8(v[u], byte_z, z, s, row[u], blk[u], lane16, live(u));
     }
-    put_block8(v[u], a, s, row[u], blk[u], lane16, live);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kEltUnroll; u += 2) {
+      int byte[2];
+      block_bytes(amax8(v[u]), amax8(v[u + 1]), byte[0], byte[1]);
+      put8(v[u], byte[0], a, s, row[u], blk[u], lane16, live(u));
+      put8(v[u + 1], byte[1], a, s, row[u + 1], blk[u + 1], lane16, live(u + 1));
+    }
   }
 }
 
@@ -167,7 +178,11 @@ __global__ void __launch_bounds__(kEltThreads, kEltCtas) gelu_bwd_kernel(const T
       for (int i = 0; i < kVec; ++i) v[u][i] = 0.f;
     }
     if (b < blocks) store8<T, VEC>(dz + (size_t)row * s.cols + col, s.cols - col, v[u]);
-    if (q.codes) put_block8(v[u], q, s, row, blk, lane16, b < blocks);
+    if (q.codes) {
+      int bits, unused;
+      block_bytes(amax8(v[u]), 0, bits, unused);
+      put8(v[u], bits, q, s, row, blk, lane16, b < blocks);
+    }
   }
 }
 
