@@ -4,7 +4,8 @@
 // Both are bound by memory.  A row is held by 1 to 16 warps, each thread with
 // one to four chunks of 8 columns, so that everything is formed from one read
 // of the inputs; what limits them is how many loads are in flight.  65536 x 1024
-// bf16 with a checkpoint: forward 86 us (6.2 TB/s of 6.7), backward 103 us
+// bf16 with a checkpoint: forward 101 us (5.3 TB/s of 6.7; 86 without the care for
+// codes on a border, which left 20 to 40 of 67 million off, now 2 to 9), backward 103 us
 // (4.5 TB/s; 101 us, 5.3 TB/s, from the full rows).
 #include <algorithm>
 #include <type_traits>
@@ -39,6 +40,32 @@ __device__ __forceinline__ float group_sum(float x, float *part) {
   return x;
 }
 
+// A sum kept as hi + lo: each addition's rounding goes into lo.
+struct Sum2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum2 operator+(const Sum2 &a, const Sum2 &b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float lo = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo), hi = s + lo;
+  return Sum2{hi, lo - (hi - s)};
+}
+
+// group_sum of such sums; `part` is used once.
+template <int W>
+__device__ __forceinline__ Sum2 group_sum2(Sum2 x, Sum2 *part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x = x + Sum2{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+  if (W == 1) return x;
+  const int warp = threadIdx.x >> 5, first = warp / W * W;
+  if ((threadIdx.x & 31) == 0) part[warp] = x;
+  __syncthreads();
+  x = part[first];
+#pragma unroll
+  for (int i = 1; i < W; ++i) x = x + part[first + i];
+  return x;
+}
+
 template <int W> struct NormCfg {
   static constexpr int kThreads = W > 8 ? 32 * W : 256;
   static constexpr int kRows = kThreads / (32 * W);  // rows in flight in a CTA
@@ -46,11 +73,33 @@ template <int W> struct NormCfg {
 
 // How many CTAs share an SM: their rows' loads are what hides the memory's
 // latency.  Forward, 65536 x 1024 bf16: 121 us with two, 97 with three, 90 with
-// four (86, 6.2 TB/s, since two blocks' scales share their shuffles); fp32 145,
-// 141, 151.  Backward: two (one was left with the 193
+// four (86 since two blocks' scales share their shuffles, 101 with the exact
+// borders of settle8); fp32 145, 141, 151.  Backward: two (one was left with the 193
 // registers that bf16 took unbounded: 296 us, 103 with two), and one for fp32.
 template <typename T, int W> constexpr int fwd_ctas() { return W > 8 ? 2 : sizeof(T) == 2 ? 4 : 3; }
 template <typename T, int W> constexpr int bwd_ctas() { return W > 8 || sizeof(T) == 4 ? 1 : 2; }
+
+// Moves those of 8 results y = v (root + rest) g by one unit of fp32 towards the
+// exact product that lie just halfway between two e4m3 codes of their scale
+// (three fraction bits and a one after them: the last 20 bits are 0x80000).
+__device__ __forceinline__ void settle8(float *y, int byte, const float *v, const float *g, float root, float rest) {
+  if (byte == kScaleNan) return;
+  const float inv = scale_inverse(byte);
+  uint32_t off[kVec], nearest = ~0u;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    off[i] = (__float_as_uint(y[i] * inv) & 0xFFFFFu) ^ 0x80000u;
+    nearest = min(nearest, off[i]);
+  }
+  if (nearest != 0) return;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const float n = v[i] * root;
+    const float left = fmaf(n, g[i], -y[i]) + fmaf(v[i], rest, fmaf(v[i], root, -n)) * g[i];
+    if (off[i] == 0 && left != 0.f)
+      y[i] = __uint_as_float(__float_as_uint(y[i]) + ((left > 0.f) == (y[i] > 0.f) ? 1u : ~0u));
+  }
+}
 
 // W warps hold a row, each thread NC chunks of 8 of its columns, in registers
 // between the sum of squares and the quantization: h and y are formed from one
@@ -59,7 +108,7 @@ template <typename T, int W, int NC, bool VEC>
 __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
     rms_norm_kernel(const T *x, const T *res, const float *gamma, float eps, T *h, float *rstd, Mat8 y, Mat8 hq,
                     Shape8 s) {
-  __shared__ float part[NormCfg<W>::kThreads / 32];
+  __shared__ Sum2 part[NormCfg<W>::kThreads / 32];
   const int l = threadIdx.x % (32 * W), lane16 = l & (kVecs - 1);
   const long long row = (long long)blockIdx.x * NormCfg<W>::kRows + threadIdx.x / (32 * W);
   const bool live = row < s.rows;
@@ -84,24 +133,36 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
       }
     }
   }
-  float ss = 0.f;
+  // The sum of squares: 8 columns at a time in plain fp32, whose roundings are
+  // many and small, and those sums without loss: the last few additions'
+  // roundings would be the whole row's.
+  Sum2 ss{0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int col = (c * 32 * W + l) * kVec;
     if (h && live) store8<T, VEC>(h + at + col, s.cols - col, v[c]);
-    float q[4];  // sums by twos: a chain's roundings would add up
+    float q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = fmaf(v[c][2 * i], v[c][2 * i], v[c][2 * i + 1] * v[c][2 * i + 1]);
-    ss += (q[0] + q[1]) + (q[2] + q[3]);
+    ss = ss + Sum2{(q[0] + q[1]) + (q[2] + q[3]), 0.f};
   }
-  const float m = group_sum<W>(ss, part) / (float)s.cols + eps;
-  const float root = 1.f / sqrtf(m);
+  ss = group_sum2<W>(ss, part);
+  const float cols = (float)s.cols, mean = ss.hi / cols;
+  const Sum2 m = Sum2{mean, (fmaf(-mean, cols, ss.hi) + ss.lo) / cols} + Sum2{eps, 0.f};
+  // a sum past fp32's range has lost its low part to inf - inf
+  const float m_hi = ss.hi < INFINITY ? m.hi : mean + eps;
+  const float root = 1.f / sqrtf(m_hi);
   if (rstd && live && l == 0) rstd[row] = root;
   // What the rounding of root left out, by one Newton step.  y is formed with
-  // it and with the rounding of its first product, so that an e4m3 code
-  // differs from the exact y's only where that lies within 2^-24 of a border.
+  // it and with the rounding of its first product; where y then lies on a
+  // border between two codes, what is left of it decides (settle8).  So an e4m3
+  // code is that of the exact y unless it is within about 2^-27 of a border.
   // (Where a product overflows the remainder is NaN, and so is the block.)
-  const float rest = m < INFINITY && root < INFINITY ? 0.5f * root * fmaf(-m * root, root, 1.f) : 0.f;
+  float rest = 0.f;
+  if (m_hi > 0.f && m_hi < INFINITY && root < INFINITY) {
+    const float sq = root * root, sq_lo = fmaf(root, root, -sq);
+    rest = 0.5f * root * (fmaf(-m_hi, sq, 1.f) - fmaf(m_hi, sq_lo, m.lo * sq));
+  }
   const float2 root2 = make_float2(root, root), rest2 = make_float2(rest, rest);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -121,6 +182,7 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
     }
     int byte_y, byte_h;
     block_bytes(amax8(out), amax8(v[c]), byte_y, byte_h);
+    settle8(out, byte_y, v[c], g, root, rest);
     put8(out, byte_y, y, s, row, blk, lane16, on);
     if (hq.codes) put8(v[c], byte_h, hq, s, row, blk, lane16, on);
   }
