@@ -4,9 +4,10 @@
 // Both are bound by memory.  A row is held by 1 to 16 warps, each thread with
 // one to four chunks of 8 columns, so that everything is formed from one read
 // of the inputs; what limits them is how many loads are in flight.  65536 x 1024
-// bf16 with a checkpoint: forward 101 us (5.3 TB/s of 6.7; 86 without the care for
-// codes on a border, which left 20 to 40 of 67 million off, now 2 to 9), backward 103 us
-// (4.5 TB/s; 101 us, 5.3 TB/s, from the full rows).
+// bf16 with a checkpoint: forward 101 us (5.3 TB/s of 6.7; 86 us without the care
+// for codes on a border, of which 2 to 9 in 67 million are off, against 15 to 42
+// where y is formed in plain fp32), backward 103 us (4.5 TB/s; 101 us, 5.3 TB/s,
+// from the full rows).
 #include <algorithm>
 #include <type_traits>
 
