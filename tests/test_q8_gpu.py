@@ -473,3 +473,31 @@ def test_offsets_past_32_bits(q8):
     for r in range(0, rows, 65536):
         dw64 += out[r:r + 65536, -8:].double().t() @ values[r:r + 65536].double()
     assert np.linalg.norm(np64(dw[-8:]) - np64(dw64)) <= 2e-6 * np.linalg.norm(np64(dw64))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [264, 1001])
+def test_gradients_in_place(q8, cols, dtype):
+    """dz may be da; dh may be dy or dres (aligned rows and rows that start anywhere)."""
+    from sub_linear_memory_gb300 import binding
+
+    rows, st = 37, torch.cuda.current_stream().cuda_stream
+    f = "" if dtype == BF16 else "_f32"
+    z, da = draw((rows, cols), 80, dtype, 2.0), draw((rows, cols), 81, dtype)
+    z8 = q8.quantize(z)
+    want, buf = q8.gelu_bwd(da, z8), da.clone()
+    call = getattr(binding.raw(), "slim_q8_gelu_bwd" + f)
+    assert call(buf.data_ptr(), z8.codes.data_ptr(), z8.scales.data_ptr(), buf.data_ptr(), None, None, rows, cols, st) == 0
+    sync()
+    assert torch.equal(buf, want)
+    gamma, rstd = 1 + 0.1 * draw((cols,), 82), torch.rand(rows, device="cuda") + 0.5
+    dres = draw((rows, cols), 83, dtype)
+    want, _ = q8.rms_norm_bwd(da, z8, rstd, gamma, dres=dres)
+    call = getattr(binding.raw(), "slim_q8_rms_norm_bwd" + f)
+    for over in ("dy", "dres"):
+        dy, dr = da.clone(), dres.clone()
+        out = dy if over == "dy" else dr
+        assert call(dy.data_ptr(), None, z8.codes.data_ptr(), z8.scales.data_ptr(), rstd.data_ptr(), gamma.data_ptr(),
+                    dr.data_ptr(), out.data_ptr(), None, None, 0, rows, cols, st) == 0
+        sync()
+        assert torch.equal(out, want)
