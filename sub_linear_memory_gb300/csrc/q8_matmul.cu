@@ -247,7 +247,7 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
 
 }  // namespace sm
 
-// ---- many output tiles: a CTA pair for each 256 x NT tile --------------------------
+// ---- more rows: a CTA pair for each 256 x 256 tile ---------------------------------
 //
 // Two SMs work on one tile (cta_group::2), each loads half of either operand,
 // so a 128-byte step of k moves 32 KB into each SM's shared memory for 512
@@ -256,15 +256,15 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
 // at a time), four warps turn the finished accumulator into rows of out while
 // the next tile is multiplied into the other one.
 //
-// 65536 x 4096 x 1024: 180 us, 3.06 PFLOP/s; 19456 x 4096 x 8192 3.35 PFLOP/s when
-// first built (1.6 and 1.8 times the measured bf16 rate; a sustained loop meets
+// 65536 x 4096 x 1024: 178 us, 3.09 PFLOP/s; 16384 x 4096 x 4096 154 us, 3.56
+// PFLOP/s (1.6 and 1.9 times the measured bf16 rate; a sustained loop meets
 // the power limit, 204 us at 1.53 GHz).  What bounds it are the operands' way
 // into shared memory, which the MMAs read at the same time, and at short k the
 // hand-over between the two accumulators.  Tiles of 192 and 128 columns were
 // slower (262 and 306 against 251 us), as they load more for each product.
 namespace lg {
 
-constexpr int kThreads = 384, kStages = 6, kTm = 256;
+constexpr int kThreads = 384, kStages = 6, kTm = 256, kTn = 256;
 constexpr uint32_t kA = kBlock * kBlock;
 constexpr uint32_t kOut = 4096;  // one warp's 32 rows x 128 bytes of out
 enum {
@@ -272,28 +272,22 @@ enum {
   S_ACCFREE = S_ACC + 2, S_DONE, S_COUNT
 };
 
-template <int NT> struct Lay {
-  static_assert(NT % kBlock == 0, "a tile's columns are whole blocks of the weight's scales");
-  static constexpr uint32_t kB = NT / 2 * kBlock, kStage = kA + kB;
-  static constexpr uint32_t kOutAt = kStages * kStage, kBar = kOutAt + 8 * kOut, kSmem = 1024 + kBar + 256;
-  // Tensor memory: two accumulators, and two sets of 12 scale columns at the
-  // end.  Two of 256 columns do not fit beside them, so they share 32 columns,
-  // which the epilogue reads first.
-  static constexpr uint32_t kSf = 480;
-  static constexpr bool kOverlap = 2 * NT > 480;
-  static constexpr uint32_t kAcc1 = kOverlap ? 480 - NT : NT;
-};
+constexpr uint32_t kB = kTn / 2 * kBlock, kStage = kA + kB;
+constexpr uint32_t kOutAt = kStages * kStage, kBar = kOutAt + 8 * kOut, kSmem = 1024 + kBar + 256;
+// Tensor memory: two accumulators, and two sets of 12 scale columns from
+// column 480 on.  Two of 256 columns do not fit beside those, so they share 32
+// columns, which the epilogue reads first.
+constexpr uint32_t kSf = 480, kAcc1 = kSf - kTn;
 
-template <int NT, bool F32>
+template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                   const __grid_constant__ CUtensorMap mo, const uint8_t *a_scales, const uint8_t *b_scales, void *out,
                   int rows, int n, int kb, int pitch, int tiles_n, int tiles, int tma_out, int *status) {
-  using LY = Lay<NT>;
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t sbase = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t *smem = raw + (sbase - smem_u32(raw));
-  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + LY::kBar);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kBar);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + S_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -340,12 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     int i = 0;
     for (int t = pair; t < tiles && ok; t += pairs) {
-      const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * NT + (int)rank * (NT / 2);
+      const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * kTn + (int)rank * (kTn / 2);
       for (int kk = 0; kk < kb; ++kk, ++i) {
         const int s = i % kStages;
         if (i >= kStages && !wait(S_EMPTY + s, (uint32_t)(i / kStages - 1) & 1)) break;
-        if (rank == 0) mbar_arrive_expect_tx(bar + S_FULL + s, 2 * LY::kStage);
-        const uint32_t full = map_peer(smem_u32(bar + S_FULL + s), 0), at = sbase + s * LY::kStage;
+        if (rank == 0) mbar_arrive_expect_tx(bar + S_FULL + s, 2 * kStage);
+        const uint32_t full = map_peer(smem_u32(bar + S_FULL + s), 0), at = sbase + s * kStage;
         tma_load_2d_pair(at, &ma, full, kk * kBlock, m0);
         tma_load_2d_pair(at + kA, &mb, full, kk * kBlock, n0);
       }
@@ -356,22 +350,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool issues = elect_lane();
     int i = 0, quad = 0, j = 0;
     for (int t = pair; t < tiles && ok; t += pairs, ++j) {
-      // the accumulator's columns are free: those it shares with the last
-      // tile's have been read, or all of the tile's before that
-      if (LY::kOverlap ? j > 0 && !wait_warp(S_ACCFREE, (uint32_t)(j - 1) & 1)
-                       : j > 1 && !wait_warp(S_ACCFREE, (uint32_t)(j - 2) & 1))
-        break;
+      // the accumulator's columns are free: those that it shares with the last
+      // tile's have been read, so all of the tile's before that too
+      if (j > 0 && !wait_warp(S_ACCFREE, (uint32_t)(j - 1) & 1)) break;
       tc_fence_after();
-      const uint32_t acc = tbase + (j & 1 ? LY::kAcc1 : 0);
+      const uint32_t acc = tbase + (j & 1 ? kAcc1 : 0);
       for (int kk = 0; kk < kb; ++kk, ++i) {
-        const uint32_t sf = tbase + LY::kSf + 12 * (quad & 1);
+        const uint32_t sf = tbase + kSf + 12 * (quad & 1);
         if ((kk & 3) == 0 && !wait_warp(S_SF + (quad & 1), (uint32_t)(quad >> 1) & 1)) break;
         const int s = i % kStages;
         if (!wait_warp(S_FULL + s, (uint32_t)(i / kStages) & 1)) break;
         tc_fence_after();
-        const uint32_t id = make_idesc_mx8(kTm, NT, kk & 3);
-        const uint64_t da = make_desc(sbase + s * LY::kStage, 16u, 1024u, kSwizzle128);
-        const uint64_t db = make_desc(sbase + s * LY::kStage + kA, 16u, 1024u, kSwizzle128);
+        const uint32_t id = make_idesc_mx8(kTm, kTn, kk & 3);
+        const uint64_t da = make_desc(sbase + s * kStage, 16u, 1024u, kSwizzle128);
+        const uint64_t db = make_desc(sbase + s * kStage + kA, 16u, 1024u, kSwizzle128);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           if (issues) mma_mx8_pair(acc, da + 2 * x, db + 2 * x, id, sf, sf + 4, kk > 0 || x > 0);
@@ -389,24 +381,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_drain(bar + S_DONE, 0);
   } else if (warp >= 4 && warp < 8) {
-    // scale words of 4 blocks of k at a time: 128 rows of a (this CTA's), NT
+    // scale words of 4 blocks of k at a time: 128 rows of a (this CTA's), kTn
     // rows of b.  The words of the next 4 blocks (of the next tile, at the end
     // of one) are on their way from memory while these wait for their columns:
     // loaded only then, a first load from DRAM would hold up the MMAs.
-    const uint32_t at0 = tmem_addr(tbase, 32u * (warp & 3), LY::kSf);
+    const uint32_t at0 = tmem_addr(tbase, 32u * (warp & 3), kSf);
     constexpr uint32_t kOnes = 0x7f7f7f7fu;
     struct Words {
-      uint32_t a[4], b[(NT + kBlock - 1) / kBlock];
+      uint32_t a[4], b[kTn / kBlock];
     };
     auto fetch = [&](int t, int kk, Words &w) {
-      const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * NT;
+      const int m0 = t / tiles_n * kTm + (int)rank * kBlock, n0 = t % tiles_n * kTn;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int m = m0 + 32 * g + lane;
         w.a[g] = m < rows ? __ldg(reinterpret_cast<const uint32_t *>(a_scales + (size_t)m * pitch + kk)) : kOnes;
       }
 #pragma unroll
-      for (int g = 0; g < (NT + kBlock - 1) / kBlock; ++g) {
+      for (int g = 0; g < kTn / kBlock; ++g) {
         const int blk = n0 / kBlock + g;
         w.b[g] = blk * kBlock < n ? __ldg(reinterpret_cast<const uint32_t *>(b_scales + (size_t)blk * pitch + kk)) : kOnes;
       }
@@ -422,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (quad >= 2 && !wait(S_SFFREE + (quad & 1), (uint32_t)((quad >> 1) - 1) & 1)) break;
         tc_fence_after();
         const uint32_t at = at0 + 12 * (quad & 1);
-        const uint32_t b0 = now.b[0], b1 = now.b[(NT - 1) / kBlock];
+        const uint32_t b0 = now.b[0], b1 = now.b[1];
         __syncwarp();
         tmem_st4u(at, now.a[0], now.a[1], now.a[2], now.a[3]);
         tmem_st4u(at + 4, b0, b0, b0, b0);
@@ -436,26 +428,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp - 8;
     const uint32_t lanes = 32u * w;
     constexpr int kCols = F32 ? 32 : 64;  // 128 bytes of a row of out
-    constexpr int kChunks = NT / kCols;
+    constexpr int kChunks = kTn / kCols;
     int j = 0, turn = 0;
     for (int t = pair; t < tiles && ok; t += pairs, ++j) {
-      const int m0 = t / tiles_n * kTm + (int)rank * kBlock + 32 * w, n0 = t % tiles_n * NT;
+      const int m0 = t / tiles_n * kTm + (int)rank * kBlock + 32 * w, n0 = t % tiles_n * kTn;
       if (!wait(S_ACC + (j & 1), (uint32_t)(j >> 1) & 1)) break;
       tc_fence_after();
-      const uint32_t acc = j & 1 ? LY::kAcc1 : 0;
+      const uint32_t acc = j & 1 ? kAcc1 : 0;
       for (int x = 0; x < kChunks; ++x) {
         // the columns shared with the other accumulator first: the last of the first, the first of the second
-        const int c = (LY::kOverlap && !(j & 1) ? kChunks - 1 - x : x) * kCols;
+        const int c = (j & 1 ? x : kChunks - 1 - x) * kCols;
         float v[kCols];
         __syncwarp();
         if constexpr (F32) tmem_ld32(tmem_addr(tbase, lanes, acc + c), v);
         else tmem_ld32x2(tmem_addr(tbase, lanes, acc + c), tmem_addr(tbase, lanes, acc + c + 32), v, v + 32);
-        if (x == (LY::kOverlap ? 0 : kChunks - 1)) {
+        if (x == 0) {
           tc_fence_before();
           arrive_leader(S_ACCFREE);
         }
         if (m0 >= rows || n0 + c >= n) continue;  // uniform over the warp
-        const uint32_t buf = sbase + LY::kOutAt + (2 * w + (turn & 1)) * kOut;
+        const uint32_t buf = sbase + kOutAt + (2 * w + (turn & 1)) * kOut;
         ++turn;
         // the store that last read this buffer is done reading
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
@@ -503,30 +495,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc_pair(tbase, 512);
 }
 
-template <int NT, bool F32>
+template <bool F32>
 cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                    int rows, int n, int k, int *status, cudaStream_t st) {
-  using LY = Lay<NT>;
   constexpr int kSize = F32 ? 4 : 2;
-  const int kb = blocks_of(k), tiles_n = (n + NT - 1) / NT;
+  const int kb = blocks_of(k), tiles_n = (n + kTn - 1) / kTn;
   const long long tiles = (((long long)rows + kTm - 1) / kTm) * tiles_n;
   const uint64_t kp = (uint64_t)kb * kBlock;
   const bool tma_out = (long long)n * kSize % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   CUtensorMap ma, mb, mo;
   if (!make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, rows, kp, kp, kBlock, kBlock, true) ||
-      !make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, n, kp, kp, NT / 2, kBlock, true))
+      !make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, n, kp, kp, kTn / 2, kBlock, true))
     return cudaErrorInvalidValue;
   mo = ma;
   if (tma_out && !make_map_2d(&mo, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, rows,
                               n, (uint64_t)n * kSize, 32, 128 / kSize, true))
     return cudaErrorInvalidValue;
-  auto kern = matmul_kernel<NT, F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::kSmem);
+  auto kern = matmul_kernel<F32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(152, 2 * tiles));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = LY::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -552,8 +543,8 @@ cudaError_t matmul(const void *a_codes, const void *a_scales, const void *b_code
   // 128 rows x 4096 x 1024 8.2 against 7.2 (64 rows 5.9), 512 rows 12.2 against
   // 7.3 when the split kernel took more rows.
   if (rows > kBlock || (rows > kBlock / 2 && k <= 1024))
-    return f32 ? lg::launch<256, true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
-               : lg::launch<256, false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
+    return f32 ? lg::launch<true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
+               : lg::launch<false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
   return f32 ? sm::launch<true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
              : sm::launch<false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);
 }
