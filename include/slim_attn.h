@@ -372,7 +372,9 @@ slim_status slim_q8_pack_weight_f32(const float *w, void *codes, void *scales, v
  * h: NULL, or [rows][cols] (may be x or res).  rstd: NULL, or fp32 [rows].
  * gamma: fp32 [cols].  h_codes, h_scales: NULL, or the 8-bit checkpoint of h
  * for the backward.  1 <= cols <= 16384, else SLIM_ERR_INVALID_ARG or
- * SLIM_ERR_UNSUPPORTED; eps >= 0. */
+ * SLIM_ERR_UNSUPPORTED; eps >= 0.  A row whose sum of squares is past fp32's
+ * range (an infinity, or |h| over about 1.8e19 / sqrt(cols)) has rstd = 0, and
+ * y = 0 but in the blocks that hold an infinity, which are NaN. */
 slim_status slim_q8_rms_norm(const void *x, const void *res, const float *gamma, float eps, void *h, float *rstd,
                              void *y_codes, void *y_scales, void *h_codes, void *h_scales, int rows, int cols,
                              slim_stream_t stream);

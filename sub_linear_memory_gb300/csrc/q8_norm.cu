@@ -8,6 +8,8 @@
 // for codes on a border, of which 2 to 9 in 67 million are off, against 15 to 42
 // where y is formed in plain fp32), backward 103 us (4.5 TB/s; 101 us, 5.3 TB/s,
 // from the full rows).
+#include <cfloat>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -41,13 +43,16 @@ __device__ __forceinline__ float group_sum(float x, float *part) {
   return x;
 }
 
-// A sum kept as hi + lo: each addition's rounding goes into lo.
+// A sum kept as hi + lo: each addition's rounding goes into lo.  Where the sum
+// is past fp32's range its rounding is inf - inf; fmaxf takes the number
+// instead of that NaN, so hi is the infinity of a plain sum (and a NaN only
+// where an operand's hi is one).
 struct Sum2 {
   float hi, lo;
 };
 __device__ __forceinline__ Sum2 operator+(const Sum2 &a, const Sum2 &b) {
   const float s = a.hi + b.hi, t = s - a.hi;
-  const float lo = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo), hi = s + lo;
+  const float lo = fmaxf((a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo), -FLT_MAX), hi = s + lo;
   return Sum2{hi, lo - (hi - s)};
 }
 
@@ -150,19 +155,19 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
   ss = group_sum2<W>(ss, part);
   const float cols = (float)s.cols, mean = ss.hi / cols;
   const Sum2 m = Sum2{mean, (fmaf(-mean, cols, ss.hi) + ss.lo) / cols} + Sum2{eps, 0.f};
-  // a sum past fp32's range has lost its low part to inf - inf
-  const float m_hi = ss.hi < INFINITY ? m.hi : mean + eps;
-  const float root = 1.f / sqrtf(m_hi);
+  const float root = 1.f / sqrtf(m.hi);  // 0 where the sum is past fp32's range
   if (rstd && live && l == 0) rstd[row] = root;
   // What the rounding of root left out, by one Newton step.  y is formed with
   // it and with the rounding of its first product; where y then lies on a
   // border between two codes, what is left of it decides (settle8).  So an e4m3
   // code is that of the exact y unless it is within about 2^-27 of a border.
   // (Where a product overflows the remainder is NaN, and so is the block.)
+  // No step where root is 0, or so large that its square is past fp32's range.
   float rest = 0.f;
-  if (m_hi > 0.f && m_hi < INFINITY && root < INFINITY) {
-    const float sq = root * root, sq_lo = fmaf(root, root, -sq);
-    rest = 0.5f * root * (fmaf(-m_hi, sq, 1.f) - fmaf(m_hi, sq_lo, m.lo * sq));
+  const float sq = root * root;
+  if (m.hi < INFINITY && sq < INFINITY) {
+    const float sq_lo = fmaf(root, root, -sq);
+    rest = 0.5f * root * (fmaf(-m.hi, sq, 1.f) - fmaf(m.hi, sq_lo, m.lo * sq));
   }
   const float2 root2 = make_float2(root, root), rest2 = make_float2(rest, rest);
 #pragma unroll

@@ -1,0 +1,81 @@
+"""GPU tests of the 8-bit layer operators at the ends of their ranges, against
+fp64: values past what fp32 can square, long sums, many tiles."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q8 as ref
+from sub_linear_memory_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def q8():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from sub_linear_memory_gb300 import q8
+
+    return q8
+
+
+def sync():
+    from sub_linear_memory_gb300 import binding
+
+    binding.sync_status()
+
+
+def np64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def draw(shape, slot, dtype=F32, scale=1.0):
+    return inputs.gaussian(shape, 7500, slot, scale=scale, dtype=dtype).cuda()
+
+
+# ---- norm: sums of squares past fp32's range ----------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [40, 264, 1000, 1024, 3001, 16384])
+def test_rms_norm_past_fp32_range(q8, cols, dtype):
+    """Rows of finite values whose squares overflow have rstd = 0 and y = 0, an
+    infinity is NaN in its own block, a NaN in its whole row; a row whose
+    1 / rms is finite but not its square is normed as any other."""
+    x = draw((9, cols), 1, dtype)
+    x[1] = 1e20
+    x[2, cols // 2] = -2e19  # one square that overflows
+    x[3] = 1.7e19 * cols ** -0.25  # the sum alone overflows
+    x[4, cols - 1] = float("inf")
+    x[5, 3] = float("nan")
+    tiny = torch.where(draw((cols,), 2) < 0, -1e-20, 1e-20)
+    x[6] = tiny.to(dtype)
+    gamma = 1 + 0.1 * draw((cols,), 3)
+    for checkpoint in (False, True):
+        h, y, rstd, h8 = q8.rms_norm(x, gamma, eps=0.0, checkpoint=checkpoint)
+        sync()
+        v, r = np64(q8.dequantize(y)), np64(rstd)
+        over = [1, 2] if cols < 16 else [1, 2, 3]
+        assert np.all(r[over] == 0) and np.all(v[over] == 0)
+        own = np.arange(cols) // 128 == (cols - 1) // 128
+        assert r[4] == 0 and np.isnan(v[4][own]).all() and np.all(v[4][~own] == 0)
+        assert np.isnan(r[5]) and np.isnan(v[5]).all()
+        # squares of 1e-40 are held to 2^-150, 2^-17 of themselves, and so is their mean
+        h64 = np64(x[6])
+        assert abs(r[6] * np.sqrt((h64 * h64).mean()) - 1) <= 2.0 ** -16
+        want = h64 / np.sqrt((h64 * h64).mean()) * np64(gamma)
+        step = 2.0 ** (np64(y.scales[6:7].double())[0, np.arange(cols) // 128] - 127 - 10)
+        assert np.all(np.abs(v[6] - want) <= np.maximum(np.abs(want) * 2.0 ** -4, step) * (1 + 2.0 ** -14))
+        # the rows beside them are untouched
+        rest = [0, 7, 8]
+        assert torch.equal(rstd[rest], q8.rms_norm(x[rest], gamma, eps=0.0)[2])
+        if checkpoint:
+            dh, dgamma = q8.rms_norm_bwd(draw((9, cols), 4, dtype), h8, torch.where(rstd.isnan(), 0, rstd), gamma)
+            sync()
+            assert torch.isfinite(dh[[0, 1, 2, 3, 7, 8]]).all()
+    # the same without eps in the row's way
+    r = q8.rms_norm(x, gamma, eps=1e-5)[2]
+    sync()
+    assert np.all(np64(r)[over] == 0) and abs(float(r[6]) - 1e-5 ** -0.5) < 1e-3
+    assert float(q8.rms_norm(x, gamma, eps=float("inf"))[2][0]) == 0
