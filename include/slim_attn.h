@@ -419,7 +419,12 @@ slim_status slim_q8_gelu_bwd_f32(const float *da, const void *z_codes, const voi
 
 /* out [rows][n] = a [rows][k] . b [n][k]^T: a with R = 1, b a packed weight
  * (R = 128).  Products and sums in fp32 on the tensor cores (tcgen05, scales
- * applied per 128 columns), rounded once to out.  Rows past `rows` and columns
+ * applied per 128 columns), which truncate as they add, four times in 128
+ * columns: a sum of terms of one sign loses 1.5e-6 of itself at k = 4096.  An
+ * fp32 result adds sums of 4096 columns with rounding to nearest, so it loses
+ * no more at any k (where k > 4096, such sums under 2^-126 may count as 0).  A
+ * bf16 result rounds one sum of all k, which loses 1e-5 at k = 16384 and
+ * 1.6e-4, a twelfth of that rounding, at 131072.  Rows past `rows` and columns
  * past n of the buffers are never read or written.  k = 0 gives zeros.
  * k <= 131072, rows and n <= 8388480, else SLIM_ERR_UNSUPPORTED.
  * Data gradient: a = 8 bits of dY, b = the transposed packed weight. */

@@ -4,8 +4,16 @@
 //
 // The tensor cores multiply e4m3 codes and apply the scales themselves
 // (kind::mxf8f6f4, one E8M0 scale for each row and 32 columns: the four 32s of
-// a 128-column block read the same byte), so partial sums never leave the fp32
-// accumulator between blocks.
+// a 128-column block read the same byte), so partial sums need not leave the
+// fp32 accumulator between blocks.
+//
+// Rounding: the tensor cores add into that accumulator with truncation, four
+// times a block.  For operands of one sign (|normal| numbers) that takes 1.5e-6
+// of the result for k = 4096, 9.9e-6 for 16384 and 1.6e-4 for 131072.  An fp32
+// result is therefore the sum, with rounding to nearest, of parts of 32 blocks
+// each: 1.5e-6 at every k (8192 x 4096 x 8192 then takes 178 us, 165 with one
+// accumulator; 4096 x 4096 x 16384 190 and 171).  A bf16 result keeps one
+// accumulator: its own rounding is 2^-8.
 #include <algorithm>
 
 #include "kernels.h"
@@ -16,6 +24,12 @@
 namespace slim {
 namespace q8 {
 namespace {
+
+constexpr int kSumBlocks = 32;  // blocks of k that go into one accumulator where out is fp32
+// The end of the part of k that starts at block k0 of kb.
+template <bool F32> __device__ __forceinline__ int part_end(int k0, int kb) {
+  return F32 && kb - k0 > kSumBlocks ? k0 + kSumBlocks : kb;
+}
 
 // ---- few rows: weights as the MMA's M side, k split over a cluster ----------------
 //
@@ -30,7 +44,9 @@ namespace {
 namespace sm {
 
 constexpr int kThreads = 256, kStages = 4, kMaxQuads = 48;
-enum { S_FULL = 0, S_EMPTY = S_FULL + kStages, S_SF = S_EMPTY + kStages, S_DONE, S_COUNT };
+enum {
+  S_FULL = 0, S_EMPTY = S_FULL + kStages, S_SF = S_EMPTY + kStages, S_PART, S_PARTFREE, S_DONE, S_COUNT
+};
 constexpr uint32_t kW = kBlock * kBlock;  // bytes of a weight tile
 
 __host__ __device__ constexpr uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -38,8 +54,8 @@ __host__ __device__ constexpr uint32_t stage_bytes(int nt) { return kW + (uint32
 // At least 200 KB, so that no other CTA with tensor memory shares the SM: one
 // that waited here for the columns of a CTA whose cluster waits elsewhere for
 // another's would never get them.
-__host__ __device__ constexpr uint32_t smem_bytes(int nt, bool split) {
-  return max_u32(200u << 10, 1024u + kStages * stage_bytes(nt) + (split ? (uint32_t)nt * kBlock * 4u : 0u) + 256u);
+__host__ __device__ constexpr uint32_t smem_bytes(int nt) {
+  return max_u32(200u << 10, 1024u + kStages * stage_bytes(nt) + (uint32_t)nt * kBlock * 4u + 256u);
 }
 
 template <bool F32>
@@ -53,7 +69,7 @@ __global__ void __launch_bounds__(kThreads)
   const int split = (int)gridDim.x, rank = (int)blockIdx.x;
   const uint32_t sb = stage_bytes(nt);
   float *part = reinterpret_cast<float *>(smem + kStages * sb);
-  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kStages * sb + (split > 1 ? nt * kBlock * 4 : 0));
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kStages * sb + nt * kBlock * 4);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + S_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -66,6 +82,8 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(bar + S_EMPTY + s, 1);
     }
     mbar_init(bar + S_SF, 4);
+    mbar_init(bar + S_PART, 1);
+    mbar_init(bar + S_PARTFREE, 4);
     mbar_init(bar + S_DONE, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -98,7 +116,14 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = max(0, i - kStages); j < i; ++j) mbar_drain(bar + S_FULL + j % kStages, (j / kStages) & 1);
   } else if (warp == 1 && lane == 0) {
     if (wait(S_SF, 0)) {
-      for (int i = 0; i < nk; ++i) {
+      for (int i = 0, first = 0, part_no = 0; i < nk; ++i) {
+        if (F32 && i - first == kSumBlocks) {  // the accumulator is emptied before the next block starts it anew
+          mma_commit(bar + S_PART);
+          if (!wait(S_PARTFREE, part_no & 1)) break;
+          tc_fence_after();
+          first = i;
+          ++part_no;
+        }
         const int s = i % kStages;
         if (!wait(S_FULL + s, (i / kStages) & 1)) break;
         tc_fence_after();
@@ -107,7 +132,7 @@ __global__ void __launch_bounds__(kThreads)
         const uint64_t da = make_desc(sbase + s * sb, 16u, 1024u, kSwizzle128);
         const uint64_t db = make_desc(sbase + s * sb + kW, 16u, 1024u, kSwizzle128);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_mx8(tbase, da + 2 * j, db + 2 * j, id, sf, sf + 4, i > 0 || j > 0);
+        for (int j = 0; j < 4; ++j) mma_mx8(tbase, da + 2 * j, db + 2 * j, id, sf, sf + 4, i > first || j > 0);
         mma_commit(bar + S_EMPTY + s);
       }
     }
@@ -138,17 +163,40 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + S_SF);
-    const bool full = wait(S_DONE, 0);
-    tc_fence_after();
-    const int nn = n0 + 32 * (warp & 3) + lane;
-    if (full) {
+    // The parts before the last are added up in shared memory; each thread has
+    // a weight row's elements for itself.
+    float *mine = part + 32 * (warp & 3) + lane;
+    const int parts = F32 ? (nk + kSumBlocks - 1) / kSumBlocks : 1;
+    for (int p = 0; p < parts - 1; ++p) {
+      wait(S_PART, p & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
       for (int c = 0; c < rows; c += 16) {
         float v[16];
         tmem_ld16(tmem_addr(tbase, lanes, c), v);
 #pragma unroll
+        for (int i = 0; i < 16; ++i) mine[(c + i) * kBlock] = p > 0 ? mine[(c + i) * kBlock] + v[i] : v[i];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + S_PARTFREE);
+    }
+    wait(S_DONE, 0);
+    tc_fence_after();
+    const int nn = n0 + 32 * (warp & 3) + lane;
+    if (__all_sync(0xffffffffu, ok)) {
+      for (int c = 0; c < rows; c += 16) {
+        float v[16];
+        tmem_ld16(tmem_addr(tbase, lanes, c), v);
+        if (parts > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += mine[(c + i) * kBlock];
+        }
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (split > 1) {
-            part[(c + i) * kBlock + 32 * (warp & 3) + lane] = v[i];
+            mine[(c + i) * kBlock] = v[i];
           } else if (c + i < rows && nn < n) {
             const size_t at = (size_t)(c + i) * n + nn;
             if (F32) static_cast<float *>(out)[at] = v[i];
@@ -166,13 +214,13 @@ __global__ void __launch_bounds__(kThreads)
     // the SMs, and one after the other took most of the kernel (12.3 us for 128
     // rows x 4096 x 1024).
     const int nl = 4 * lane, left = n - n0 - nl;
-    const uint32_t mine = smem_u32(part);
+    const uint32_t tile = smem_u32(part);
     if (!*abort_flag && left > 0) {
       for (int c = 8 * rank + warp; c < rows; c += 8 * split) {
         float v[8][4];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (r < split) ld_peer_v4(map_peer(mine + (uint32_t)(c * kBlock + nl) * 4u, r), v[r]);
+          if (r < split) ld_peer_v4(map_peer(tile + (uint32_t)(c * kBlock + nl) * 4u, r), v[r]);
 #pragma unroll
         for (int r = 1; r < 8; ++r)
           if (r < split) {
@@ -224,8 +272,8 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
   // four columns of out in one store
   const int wide = n % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (F32 ? 15 : 7)) == 0;
   auto kern = matmul_small_kernel<F32>;
-  const uint32_t smem = smem_bytes(nt, split > 1);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kBlock, true));
+  const uint32_t smem = smem_bytes(nt);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kBlock));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split, tiles_n);
@@ -348,14 +396,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = max(0, i - kStages); j < i; ++j) mbar_drain(bar + S_FULL + j % kStages, (uint32_t)(j / kStages) & 1);
   } else if (warp == 1 && rank == 0) {
     const bool issues = elect_lane();
+    // a tile and a part of k (all of k where out is bf16) for each accumulator
     int i = 0, quad = 0, j = 0;
-    for (int t = pair; t < tiles && ok; t += pairs, ++j) {
+    for (int t = pair, k0 = 0; t < tiles && ok; ++j) {
       // the accumulator's columns are free: those that it shares with the last
-      // tile's have been read, so all of the tile's before that too
+      // one have been read, so all of the one's before that too
       if (j > 0 && !wait_warp(S_ACCFREE, (uint32_t)(j - 1) & 1)) break;
       tc_fence_after();
       const uint32_t acc = tbase + (j & 1 ? kAcc1 : 0);
-      for (int kk = 0; kk < kb; ++kk, ++i) {
+      const int k1 = part_end<F32>(k0, kb);
+      for (int kk = k0; kk < k1; ++kk, ++i) {
         const uint32_t sf = tbase + kSf + 12 * (quad & 1);
         if ((kk & 3) == 0 && !wait_warp(S_SF + (quad & 1), (uint32_t)(quad >> 1) & 1)) break;
         const int s = i % kStages;
@@ -366,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t db = make_desc(sbase + s * kStage + kA, 16u, 1024u, kSwizzle128);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (issues) mma_mx8_pair(acc, da + 2 * x, db + 2 * x, id, sf, sf + 4, kk > 0 || x > 0);
+          if (issues) mma_mx8_pair(acc, da + 2 * x, db + 2 * x, id, sf, sf + 4, kk > k0 || x > 0);
         if (issues) mma_commit_pair(bar + S_EMPTY + s);
         if ((kk & 3) == 3 || kk == kb - 1) {
           if (issues) mma_commit_pair(bar + S_SFFREE + (quad & 1));
@@ -376,6 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && issues) mma_commit_pair(bar + S_ACC + (j & 1));
       __syncwarp();
+      k0 = k1 < kb ? k1 : 0;
+      if (k0 == 0) t += pairs;
     }
     if (issues) mma_commit_pair(bar + S_DONE);
     __syncwarp();
@@ -430,11 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCols = F32 ? 32 : 64;  // 128 bytes of a row of out
     constexpr int kChunks = kTn / kCols;
     int j = 0, turn = 0;
-    for (int t = pair; t < tiles && ok; t += pairs, ++j) {
+    for (int t = pair, k0 = 0; t < tiles && ok; ++j) {
       const int m0 = t / tiles_n * kTm + (int)rank * kBlock + 32 * w, n0 = t % tiles_n * kTn;
       if (!wait(S_ACC + (j & 1), (uint32_t)(j >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t acc = j & 1 ? kAcc1 : 0;
+      // the parts of k after the first are added to out, each once the part
+      // before it has been written (single elements: by the same thread)
+      const bool add = k0 > 0;
+      if (add && tma_out && lane == 0) tma_store_wait_all();
       for (int x = 0; x < kChunks; ++x) {
         // the columns shared with the other accumulator first: the last of the first, the first of the second
         const int c = (j & 1 ? x : kChunks - 1 - x) * kCols;
@@ -465,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&mo, buf, n0 + c, m0);
+            if (add) tma_reduce_add_2d(&mo, buf, n0 + c, m0);
+            else tma_store_2d(&mo, buf, n0 + c, m0);
             tma_store_commit();
           }
         } else {  // rows of out that do not start on 16 bytes: coalesced stores of single elements
@@ -479,14 +536,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint8_t *from = smem + (buf - sbase) + r * 128 + (((bytes >> 4) ^ (r & 7)) << 4) + (bytes & 15);
               const size_t to = (size_t)(m0 + r) * n + n0 + c + col;
               if (col < left) {
-                if constexpr (F32) static_cast<float *>(out)[to] = *reinterpret_cast<const float *>(from);
-                else static_cast<__nv_bfloat16 *>(out)[to] = *reinterpret_cast<const __nv_bfloat16 *>(from);
+                if constexpr (F32) {
+                  const float v = *reinterpret_cast<const float *>(from);
+                  static_cast<float *>(out)[to] = add ? static_cast<float *>(out)[to] + v : v;
+                } else static_cast<__nv_bfloat16 *>(out)[to] = *reinterpret_cast<const __nv_bfloat16 *>(from);
               }
             }
           }
           __syncwarp();
         }
       }
+      const int k1 = part_end<F32>(k0, kb);
+      k0 = k1 < kb ? k1 : 0;
+      if (k0 == 0) t += pairs;
     }
     if (lane == 0) tma_store_wait_all();
   }

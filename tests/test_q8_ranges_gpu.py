@@ -79,3 +79,34 @@ def test_rms_norm_past_fp32_range(q8, cols, dtype):
     sync()
     assert np.all(np64(r)[over] == 0) and abs(float(r[6]) - 1e-5 ** -0.5) < 1e-3
     assert float(q8.rms_norm(x, gamma, eps=float("inf"))[2][0]) == 0
+
+
+# ---- products: long sums ------------------------------------------------------
+
+def values_on_gpu(q8, q):
+    return q8.dequantize(q, F32).double()
+
+
+# (rows, n, k): the kernel for few rows with k in one CTA and over a cluster, and
+# the whole-tile kernel with several tiles a pair, rows of out on and off 16 bytes
+@pytest.mark.parametrize("rows, n, k", [(3, 10240, 4096), (3, 10240, 23000), (5, 264, 131072), (128, 1001, 131072),
+                                        (50, 10001, 8200), (130, 264, 4096), (130, 264, 131072), (300, 1033, 16777),
+                                        (20000, 512, 8200), (2433, 1033, 9000)])
+def test_matmul_long_sums_are_not_truncated(q8, rows, n, k):
+    """Operands of one sign, so that what each addition cuts off adds up: at most
+    128 additions in one accumulator, which lose half a unit 2^-23 of a partial
+    sum that is half of the whole on average; then one rounding to nearest for
+    each 4096 columns, and 16 units for those within an instruction."""
+    g = torch.Generator(device="cuda").manual_seed(7600 + rows)
+    a = q8.quantize(torch.randn((rows, k), generator=g, device="cuda").abs())
+    w = q8.pack_weight(torch.randn((n, k), generator=g, device="cuda").abs(), transpose=False)[0]
+    buf = torch.full((rows * n + 512,), 7.0, device="cuda")
+    out = buf[256:256 + rows * n].view(rows, n)
+    q8.matmul(a, w, out=out)
+    sync()
+    assert torch.all(buf[:256] == 7) and torch.all(buf[256 + rows * n:] == 7)
+    want = values_on_gpu(q8, a) @ values_on_gpu(q8, w).t()
+    units = min(k / 32, 128) / 4 + k / 8192 + 16
+    err = float(((out.double() - want).abs() / want).max()) * 2 ** 23
+    assert err <= units, (err, units)
+    assert torch.equal(q8.matmul(a, w, dtype=F32), out)
