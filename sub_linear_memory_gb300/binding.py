@@ -211,6 +211,18 @@ def _ptr(t):
     return None if t is None else _vp(t.data_ptr())
 
 
+def check_device(device):
+    """The library launches on the current device, and a default stream's handle
+    is 0 on every device: tensors elsewhere would meet a kernel on the wrong GPU."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device (torch.cuda.device); got %s" % device)
+
+
+def _stream(device):
+    check_device(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _validate(q, k, v, w, extra=()):
     if q.dim() != 4:
         raise ValueError("q must be [B, H, L, d]")
@@ -257,8 +269,8 @@ def slim_attn_fwd(q, k, v, w, chunk, y=None, state_in=None, state_out=None):
         y = torch.empty_like(q)
     _check_state(state_in, b, h, d, m, q.device, "state_in")
     _check_state(state_out, b, h, d, m, q.device, "state_out")
+    stream = _stream(q.device)
     _prepare((b, h, length, d, m, chunk), False, q.device)
-    stream = torch.cuda.current_stream(q.device).cuda_stream
     if state_in is None and state_out is None:
         fn = _lib.slim_attn_fwd if q.dtype == torch.bfloat16 else _lib.slim_attn_fwd_f32
         _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(y), b, h, length, d, m, chunk, _vp(stream)),
@@ -285,8 +297,8 @@ def slim_attn_bwd(q, k, v, w, dy, chunk, want_dw=False, out=None, state_in=None,
         dq, dk, dv, dw = out
     for st, what in ((state_in, "state_in"), (g_in, "g_in"), (g_out, "g_out")):
         _check_state(st, b, h, d, m, q.device, what)
+    stream = _stream(q.device)
     _prepare((b, h, length, d, m, chunk), True, q.device)
-    stream = torch.cuda.current_stream(q.device).cuda_stream
     if state_in is None and g_in is None and g_out is None:
         fn = _lib.slim_attn_bwd if q.dtype == torch.bfloat16 else _lib.slim_attn_bwd_f32
         _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(dy), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dw),
@@ -307,7 +319,7 @@ def draw_orf(n, d, m, seed, step=0, out=None, device=None):
         out = torch.empty((n, d, m), dtype=torch.float32, device=dev)
     if out.shape != (n, d, m) or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [n, d, M] tensor")
-    stream = torch.cuda.current_stream(out.device).cuda_stream
+    stream = _stream(out.device)
     _check(_lib.slim_attn_draw_orf(_ptr(out), n, d, m, seed, step, _vp(stream)), "slim_attn_draw_orf")
     return out
 
@@ -334,9 +346,9 @@ def slim_attn_state(k, v, w, chunk, state=None):
         state = torch.empty((b, h, d + 1, m), dtype=torch.float32, device=k.device)
     if state.shape != (b, h, d + 1, m) or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous fp32 [B, H, d + 1, M] tensor")
+    stream = _stream(k.device)
     _prepare((b, h, max(length, 1), d, m, chunk), False, k.device)
     fn = _lib.slim_attn_state if k.dtype == torch.bfloat16 else _lib.slim_attn_state_f32
-    stream = torch.cuda.current_stream(k.device).cuda_stream
     _check(fn(_ptr(k), _ptr(v), _ptr(w), _ptr(state), b, h, length, d, m, chunk, _vp(stream)), "slim_attn_state")
     return state
 
@@ -354,7 +366,7 @@ def slim_attn_decode(q, k, v, w, state, y=None):
     if y is None:
         y = torch.empty_like(q)
     fn = _lib.slim_attn_decode if q.dtype == torch.bfloat16 else _lib.slim_attn_decode_f32
-    stream = torch.cuda.current_stream(q.device).cuda_stream
+    stream = _stream(q.device)
     _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(state), _ptr(y), b, h, d, m, _vp(stream)),
            "slim_attn_decode")
     return y
@@ -406,7 +418,7 @@ def lm_loss_grad(cfg, params, feature_w, tokens, chunk, grads=None, checkpoints=
         buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=params.device)
         _lm_ws[key] = buf
     loss = torch.empty((), dtype=torch.float64, device=params.device)
-    stream = torch.cuda.current_stream(params.device).cuda_stream
+    stream = _stream(params.device)
     if checkpoints is not None and checkpoints.numel() * checkpoints.element_size() < lm_checkpoint_bytes(
             cfg, b, length, chunk):
         raise ValueError("checkpoints too small")

@@ -76,6 +76,7 @@ def empty(rows, cols, block_rows=1, device=None):
 
 
 def _stream(device):
+    binding.check_device(device)
     # the stream's handle alone: torch.cuda.current_stream builds an object around it, for more
     # than a small kernel's launch costs
     return torch._C._cuda_getCurrentRawStream(device.index)
