@@ -402,8 +402,10 @@ slim_status slim_q8_rms_norm_bwd_f32(const float *dy, const float *h, const void
                                      slim_stream_t stream);
 size_t slim_q8_rms_norm_bwd_workspace_bytes(int rows, int cols);
 
-/* a = 8 bits of GeLU(z) = z Phi(z) (exact normal distribution function), and,
- * where z_codes and z_scales are not NULL, the 8-bit checkpoint of z. */
+/* a = 8 bits of GeLU(z) = z Phi(z) with the normal distribution function (not
+ * its tanh form), and, where z_codes and z_scales are not NULL, the 8-bit
+ * checkpoint of z.  Phi is within 6e-7 of its value for |z| <= 2 (with fp32
+ * rows within 8e-8 of 1 for |z| <= 1), beyond that within 6e-7 + 2^-24 z^2. */
 slim_status slim_q8_gelu(const void *z, void *a_codes, void *a_scales, void *z_codes, void *z_scales, int rows,
                          int cols, slim_stream_t stream);
 slim_status slim_q8_gelu_f32(const float *z, void *a_codes, void *a_scales, void *z_codes, void *z_scales, int rows,

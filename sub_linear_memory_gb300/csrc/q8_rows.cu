@@ -5,8 +5,8 @@
 // neighbouring threads hold one block of 128 columns in registers while they
 // agree on its scale (four shuffles for two blocks).  Quantize and dequantize
 // are bound by memory (32768 x 4096 bf16: 72 us, 5.6 TB/s, and 63 us, 6.4 TB/s);
-// GeLU and its backward by their arithmetic (65536 x 1024: 76 and 70 us; without
-// it 60 and 57).
+// GeLU and its backward by their arithmetic (65536 x 1024 bf16: 76 and 70 us;
+// without it 60 and 57; fp32 88 us, and the backward 93, 6.5 TB/s).
 #include "kernels.h"
 #include "q8.h"
 #include "q8_common.cuh"
@@ -30,29 +30,47 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 // beyond |z| is exp(-z^2 / 2) times a polynomial in u = 1 / (1 + 0.35 |z|) (the
 // form of Hastings, Approximations for Digital Computers, 1955), of degree 9
 // without a constant term, fitted for the smallest relative error over
-// 0 <= |z| <= 14 (3e-8; 3e-7 with its roundings), so that the left tail keeps
-// its digits.  One exponential and one reciprocal serve both functions; the
-// polynomial runs on two values at a time.  normcdff and expf in its place
-// made GeLU 3.5 times as long as its memory traffic.
+// 0 <= |z| <= 14 (3e-8), so that the left tail keeps its digits.  With its
+// roundings the function is within 6e-7 of its value for |z| <= 2 (most of it
+// the reciprocal's unit, 2.3 times over near 0); beyond, the exponent's
+// roundings take up to z^2 units 2^-24 (8e-6 at 13).  One exponential and one
+// reciprocal serve both functions; the polynomial runs on two values at a time.
+// normcdff and expf in its place made GeLU 3.5 times as long as its memory
+// traffic.
+//
+// NEAR: for |z| <= 1 the function is 1/2 + z P(z^2) instead, P of degree 4
+// (fitted to 3e-8 of the smaller of the two tails), which is within 1.25 *
+// 2^-24.  fp32 rows take it.  bf16 rows do not: their gradient is rounded to
+// 2^-8, and 65536 x 1024 would take 88 us and 82 back for 77 and 70.
+template <bool NEAR>
 __device__ __forceinline__ void normal_parts(float2 z, float2 &cdf, float2 &pdf) {
   const float2 t = make_float2(fabsf(z.x), fabsf(z.y));
   const float2 d = __ffma2_rn(t, make_float2(0.35f, 0.35f), make_float2(1.f, 1.f));
   const float2 u = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
   float2 p = make_float2(-0.029146051f, -0.029146051f);
-  auto step = [&](float c) { p = __ffma2_rn(p, u, make_float2(c, c)); };
-  step(0.14397228f);
-  step(-0.25571546f);
-  step(0.1591755f);
-  step(-0.023110742f);
-  step(0.10550838f);
-  step(0.11983278f);
-  step(0.13986188f);
-  step(0.13962141f);
+  auto step = [](float2 &y, float2 x, float c) { y = __ffma2_rn(y, x, make_float2(c, c)); };
+  step(p, u, 0.14397228f);
+  step(p, u, -0.25571546f);
+  step(p, u, 0.1591755f);
+  step(p, u, -0.023110742f);
+  step(p, u, 0.10550838f);
+  step(p, u, 0.11983278f);
+  step(p, u, 0.13986188f);
+  step(p, u, 0.13962141f);
   p = __fmul2_rn(p, u);
-  const float2 a = __fmul2_rn(__fmul2_rn(t, t), make_float2(-0.72134752f, -0.72134752f));
+  const float2 sq = __fmul2_rn(t, t), a = __fmul2_rn(sq, make_float2(-0.72134752f, -0.72134752f));
   const float2 e = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
   const float2 q = __fmul2_rn(p, e);
   cdf = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
+  if constexpr (NEAR) {
+    float2 n = make_float2(9.15123965e-05f, 9.15123965e-05f);
+    step(n, sq, -0.00116311491f);
+    step(n, sq, 0.0099623967f);
+    step(n, sq, -0.0664881989f);
+    step(n, sq, 0.398942143f);
+    n = __ffma2_rn(n, z, make_float2(0.5f, 0.5f));
+    cdf = make_float2(t.x <= 1.f ? n.x : cdf.x, t.y <= 1.f ? n.y : cdf.y);
+  }
   pdf = __fmul2_rn(e, make_float2(0.39894228f, 0.39894228f));
 }
 
@@ -86,7 +104,7 @@ __global__ void __launch_bounds__(kEltThreads, kEltCtas) quantize_kernel(const T
 #pragma unroll
       for (int i = 0; i < kVec; i += 2) {
         float2 cdf, pdf;
-        normal_parts(make_float2(v[u][i], v[u][i + 1]), cdf, pdf);
+        normal_parts<sizeof(T) == 4>(make_float2(v[u][i], v[u][i + 1]), cdf, pdf);
         act[i] = v[u][i] * cdf.x;
         act[i + 1] = v[u][i + 1] * cdf.y;
       }
@@ -167,7 +185,7 @@ __global__ void __launch_bounds__(kEltThreads, kEltCtas) gelu_bwd_kernel(const T
 #pragma unroll
     for (int i = 0; i < kVec; i += 2) {
       float2 cdf, pdf;
-      normal_parts(make_float2(z[i], z[i + 1]), cdf, pdf);
+      normal_parts<sizeof(T) == 4>(make_float2(z[i], z[i + 1]), cdf, pdf);
       // the 8 bits are those of dz as it is stored
       v[u][i] = rounded<T>(v[u][i] * fmaf(z[i], pdf.x, cdf.x));
       v[u][i + 1] = rounded<T>(v[u][i + 1] * fmaf(z[i + 1], pdf.y, cdf.y));

@@ -110,3 +110,28 @@ def test_matmul_long_sums_are_not_truncated(q8, rows, n, k):
     err = float(((out.double() - want).abs() / want).max()) * 2 ** 23
     assert err <= units, (err, units)
     assert torch.equal(q8.matmul(a, w, dtype=F32), out)
+
+
+# ---- GeLU: the normal distribution function near 0 --------------------------------
+
+def test_gelu_slope_near_zero(q8):
+    """Phi(z) + z phi(z) in fp32 at every code with |z| <= 1 under 16 scales.
+    Phi is 1/2 + z P: within 3e-8 of Phi(-|z|) by its fit, half a unit 2^-25 of
+    P <= 0.4 and of the last step before it, and half a unit of the sum: 1.25 *
+    2^-24.  phi: two units 2^-23 of the hardware's exponential and one each of
+    the square, the exponent and the product."""
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes = codes[(codes & 127) != 127]  # without the NaNs
+    raw = torch.zeros((16, 256), dtype=torch.uint8)
+    raw[:, :254] = codes
+    scales = torch.full((16, 4), 127, dtype=torch.uint8)
+    scales[:, :2] = 127 - 1 - torch.arange(16, dtype=torch.uint8)[:, None]
+    z8 = q8.Q8(raw.view(torch.float8_e4m3fn).cuda(), scales.cuda(), 254)
+    dz = q8.gelu_bwd(torch.ones((16, 254), device="cuda"), z8)
+    sync()
+    z = np64(q8.dequantize(z8, F32))
+    near = np.abs(z) <= 1
+    assert near.sum() > 2000
+    want = ref.gelu_slope(z)
+    bound = 1.25 * 2.0 ** -24 + np.abs(z) * np.exp(-0.5 * z * z) * 0.4 * 5 * 2.0 ** -23 + 2.0 ** -24 * np.abs(want)
+    assert np.all((np.abs(np64(dz) - want) <= bound)[near]), float((np.abs(np64(dz) - want) / bound)[near].max())
