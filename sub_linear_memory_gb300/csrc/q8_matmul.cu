@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         now = next;
         if (kk + 4 < kb) fetch(t, kk + 4, next);
         else if (t + pairs < tiles) fetch(t + pairs, 0, next);
-        if (quad >= 2 && !wait(S_SFFREE + (quad & 1), (uint32_t)((quad >> 1) - 1) & 1)) break;
+        if (quad >= 2 && !wait_warp(S_SFFREE + (quad & 1), (uint32_t)((quad >> 1) - 1) & 1)) break;
         tc_fence_after();
         const uint32_t at = at0 + 12 * (quad & 1);
         const uint32_t b0 = now.b[0], b1 = now.b[1];
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int j = 0, turn = 0;
     for (int t = pair, k0 = 0; t < tiles && ok; ++j) {
       const int m0 = t / tiles_n * kTm + (int)rank * kBlock + 32 * w, n0 = t % tiles_n * kTn;
-      if (!wait(S_ACC + (j & 1), (uint32_t)(j >> 1) & 1)) break;
+      if (!wait_warp(S_ACC + (j & 1), (uint32_t)(j >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t acc = j & 1 ? kAcc1 : 0;
       // the parts of k after the first are added to out, each once the part
