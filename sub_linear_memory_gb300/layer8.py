@@ -37,6 +37,7 @@ class Layer8:
     def __init__(self, heads, w, wqkv, wo, w1, w2, g1, g2, chunk=128, eps=1e-5):
         self.heads, self.w, self.chunk, self.eps = heads, w, chunk, eps
         self.g1, self.g2 = g1, g2
+        self.d = g1.shape[0] // heads
         self.load(wqkv=wqkv, wo=wo, w1=w1, w2=w2)
 
     def load(self, **weights):
@@ -50,8 +51,8 @@ class Layer8:
 
     def _split(self, qkv, b):
         """[B L][3 heads d] -> q, k, v [B, heads, L, d]."""
-        length = qkv.shape[0] // b
-        parts = qkv.view(b, length, 3, self.heads, -1).permute(2, 0, 3, 1, 4).contiguous()
+        length = qkv.shape[0] // b if b else 0
+        parts = qkv.view(b, length, 3, self.heads, self.d).permute(2, 0, 3, 1, 4).contiguous()
         return parts[0], parts[1], parts[2]
 
     @staticmethod
@@ -83,7 +84,7 @@ class Layer8:
         grads["wo"] = q8.wgrad(dh2, o)
         q, k, v = self._split(q8.matmul(y, self.wqkv), b)
         do = q8.matmul(q8.quantize(dh2), self.wo_t)
-        do = do.view(b, -1, self.heads, q.shape[-1]).transpose(1, 2).contiguous()
+        do = do.view(b, q.shape[2], self.heads, self.d).transpose(1, 2).contiguous()
         dq, dk, dv, _ = binding.slim_attn_bwd(q, k, v, self.w, do, self.chunk)
         dqkv = torch.cat([self._rows(t) for t in (dq, dk, dv)], dim=1)
         grads["wqkv"] = q8.wgrad(dqkv, y)
@@ -100,9 +101,9 @@ class Layer8:
     def decode(self, x, r, state):
         """One token for each of B sequences: x, r [B][d_model]; state is advanced in place."""
         h, y, _, _ = q8.rms_norm(x, self.g1, res=r, eps=self.eps)
-        qkv = q8.matmul(y, self.wqkv).view(x.shape[0], 3, self.heads, -1).transpose(0, 1).contiguous()
+        qkv = q8.matmul(y, self.wqkv).view(x.shape[0], 3, self.heads, self.d).transpose(0, 1).contiguous()
         out = binding.slim_attn_decode(qkv[0], qkv[1], qkv[2], self.w, state)
-        return self._finish(h, out.view(x.shape[0], -1))
+        return self._finish(h, out.view(x.shape[0], self.heads * self.d))
 
     def _finish(self, h, o):
         p = q8.matmul(q8.quantize(o), self.wo)

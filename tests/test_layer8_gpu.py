@@ -122,3 +122,27 @@ def test_new_weights():
     assert torch.equal(f, -g)
     with pytest.raises(ValueError):
         layer.load(g1=w["g1"].cuda())
+
+
+@pytest.mark.parametrize("favor", [True, False])
+def test_no_rows(favor):
+    """Sequences of no rows, and no sequences: nothing out, gradients of zero, a state of zero."""
+    from sub_linear_memory_gb300 import binding
+    from sub_linear_memory_gb300.layer8 import Layer8
+
+    w, fw = weights(favor)
+    layer = Layer8(HEADS, fw, **{k: v.cuda() for k, v in w.items()}, chunk=64)
+    none = torch.empty((0, DM), dtype=torch.bfloat16, device="cuda")
+    for b in (2, 0):
+        (h2, f), kept = layer.forward(none, none, b)
+        dx, grads = layer.backward(none, none, kept)
+        binding.sync_status()
+        assert h2.shape == f.shape == dx.shape == (0, DM)
+        for name, want in w.items():
+            assert grads[name].shape == want.shape and bool((grads[name] == 0).all()), name
+        (h2, f), state = layer.prefill(none, none, b)
+        binding.sync_status()
+        assert h2.shape == f.shape == (0, DM) and state.shape[0] == b and bool((state == 0).all())
+    h2, f = layer.decode(none, none, state)
+    binding.sync_status()
+    assert h2.shape == f.shape == (0, DM)
