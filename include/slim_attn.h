@@ -333,7 +333,9 @@ slim_status slim_attn_decode_f32(const float *q, const float *k, const float *v,
  * A power of two makes every value exact in bf16 (and the range of e keeps it
  * a normal bf16 number), and lets the tensor cores apply the scales.  A block
  * that holds an infinity or a NaN has scale 255 and is NaN throughout, so an
- * overflow is never hidden by a saturated code.
+ * overflow is never hidden by a saturated code.  Codes that come from elsewhere
+ * have to keep to that: a NaN code under another scale is not seen by every
+ * operator (slim_q8_wgrad takes it for 480).
  *
  * rows, cols, n, k >= 0 (else SLIM_ERR_INVALID_ARG).  A call with nothing to
  * write is a no-op.  Entry points take bf16 rows, or fp32 ones with _f32;
@@ -426,7 +428,7 @@ slim_status slim_q8_gelu_bwd_f32(const float *da, const void *z_codes, const voi
  * fp32 result adds sums of 4096 columns with rounding to nearest, so it loses
  * no more at any k (where k > 4096, such sums under 2^-126 may count as 0).  A
  * bf16 result rounds one sum of all k, which loses 1e-5 at k = 16384 and
- * 1.6e-4, a twelfth of that rounding, at 131072.  Rows past `rows` and columns
+ * 1.6e-4, a 24th of that rounding, at 131072.  Rows past `rows` and columns
  * past n of the buffers are never read or written.  k = 0 gives zeros.
  * k <= 131072, rows and n <= 8388480, else SLIM_ERR_UNSUPPORTED.
  * Data gradient: a = 8 bits of dY, b = the transposed packed weight. */

@@ -600,10 +600,14 @@ cudaError_t launch(const void *a_codes, const void *a_scales, const void *b_code
 
 cudaError_t matmul(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                    bool f32, int rows, int n, int k, int *status, cudaStream_t st) {
-  // Few rows go to the split kernel, with 128 of them 8.9 us for 1024 x 4096
-  // against 13.3 with whole tiles.  Where k is short there is little to split:
-  // 128 rows x 4096 x 1024 8.2 against 7.2 (64 rows 5.9), 512 rows 12.2 against
-  // 7.3 when the split kernel took more rows.
+  // Few rows go to the split kernel, with 128 of them 8.6 us for 1024 x 4096
+  // against 13.3 with whole tiles.  Where k is short there is little to split, and
+  // what the split kernel does for each row counts, whatever n: for k = 512 and n
+  // from 128 to 4096, 65 rows 6.1-6.5 us against 5.2-5.7 with whole tiles, 128 rows
+  // 7.9-8.2 against 5.3-5.9; for k = 1024 6.2-6.5 against 6.4-6.9 and 7.4-8.0
+  // against 6.6-7.1; for k = 1536 6.4-6.8 against 7.4-8.0 and 7.7-8.3 against
+  // 7.6-8.1.  512 rows x 4096 x 1024 took 12.2 against 7.3 when the split kernel
+  // took more rows.
   if (rows > kBlock || (rows > kBlock / 2 && k <= 1024))
     return f32 ? lg::launch<true>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st)
                : lg::launch<false>(a_codes, a_scales, b_codes, b_scales, out, rows, n, k, status, st);

@@ -4,10 +4,13 @@
 // Both are bound by memory.  A row is held by 1 to 16 warps, each thread with
 // one to four chunks of 8 columns, so that everything is formed from one read
 // of the inputs; what limits them is how many loads are in flight.  65536 x 1024
-// bf16 with a checkpoint: forward 101 us (5.3 TB/s of 6.7; 86 us without the care
-// for codes on a border, of which 2 to 9 in 67 million are off, against 15 to 42
-// where y is formed in plain fp32), backward 103 us (4.5 TB/s; 101 us, 5.3 TB/s,
-// from the full rows).
+// bf16 with a checkpoint: forward 102 us (5.3 TB/s of 6.7; 86 us without the care
+// for codes on a border, of which 1 to 9 in 67 million are off, against 25 to 50
+// where y is formed in plain fp32; issue slots 76% used), backward 104 us (4.5
+// TB/s, at 128 registers with spills in the row loop; 101 us, 5.3 TB/s, from the
+// full rows).  fp32: forward 142 us (6.6 TB/s), backward 165 (5.3) and 190 (5.6).
+// Rows whose width is no multiple of 8 columns, or that do not start on 16
+// bytes, go element by element: 65536 x 1001 bf16 236 us, backward 271 and 309.
 #include <cfloat>
 
 #include <algorithm>
@@ -78,16 +81,18 @@ template <int W> struct NormCfg {
 };
 
 // How many CTAs share an SM: their rows' loads are what hides the memory's
-// latency.  Forward, 65536 x 1024 bf16: 121 us with two, 97 with three, 90 with
-// four (86 since two blocks' scales share their shuffles, 101 with the exact
-// borders of settle8); fp32 145, 141, 151.  Backward: two (one was left with the 193
-// registers that bf16 took unbounded: 296 us, 103 with two), and one for fp32.
+// latency.  Forward, 65536 x 1024 bf16: 132 us with two, 110 with three, 102 with
+// four; fp32 154, 142, 154.  Backward from the checkpoint: bf16 145 us with one,
+// 104 with two; fp32 165 with one, 214 with two.
 template <typename T, int W> constexpr int fwd_ctas() { return W > 8 ? 2 : sizeof(T) == 2 ? 4 : 3; }
 template <typename T, int W> constexpr int bwd_ctas() { return W > 8 || sizeof(T) == 4 ? 1 : 2; }
 
 // Moves those of 8 results y = v (root + rest) g by one unit of fp32 towards the
 // exact product that lie just halfway between two e4m3 codes of their scale
 // (three fraction bits and a one after them: the last 20 bits are 0x80000).
+// Two kinds of border are left as y in fp32 has them: those between codes under
+// 2^-6 of the scale, whose steps do not shrink with them, and the scale's own,
+// 448 * 2^e, which is settled before this.
 __device__ __forceinline__ void settle8(float *y, int byte, const float *v, const float *g, float root, float rest) {
   if (byte == kScaleNan) return;
   const float inv = scale_inverse(byte);
@@ -159,8 +164,9 @@ __global__ void __launch_bounds__(NormCfg<W>::kThreads, fwd_ctas<T, W>())
   if (rstd && live && l == 0) rstd[row] = root;
   // What the rounding of root left out, by one Newton step.  y is formed with
   // it and with the rounding of its first product; where y then lies on a
-  // border between two codes, what is left of it decides (settle8).  So an e4m3
-  // code is that of the exact y unless it is within about 2^-27 of a border.
+  // border between two codes, what is left of it decides (settle8).  So a normal
+  // e4m3 code is that of the exact y, under the scale of the block's largest y in
+  // fp32, unless it is within about 2^-27 of a border.
   // (Where a product overflows the remainder is NaN, and so is the block.)
   // No step where root is 0, or so large that its square is past fp32's range.
   float rest = 0.f;

@@ -31,6 +31,9 @@
 // Bound: 377 us for 65536 x 1024 x 4096, 1.46 PFLOP/s, 77% of the measured bf16
 // rate.  A step's MMAs take 512 cycles; the conversion of its codes, on the
 // integer pipe and in the shared memory that the MMAs read, holds it to 730.
+// Rows of dy that do not start on 16 bytes are loaded element by element by the
+// converting warps, which then bound it: 65536 x 1001 x 1024 957 us, against 99
+// with 1024 columns.
 #include <algorithm>
 
 #include "kernels.h"
@@ -153,7 +156,8 @@ struct Walk {
 // seven other bits at the bottom of the exponent and the top of the fraction,
 // i.e. the value times 2^-120 (the exponent biases are 7 and 127; subnormal
 // codes become subnormal bf16 numbers).  Taking alternate codes needs no byte
-// permutation, and the left shifts are multiplications, so that the integer
+// permutation (a NaN code, which stands in NaN blocks only, becomes 480: the
+// block's factor is NaN), and the left shifts are multiplications, so that the integer
 // pipe, which bounds the conversion, has five operations for four codes (with
 // a permutation for each pair it had eight, and a step took 1030 cycles).
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t &even, uint32_t &odd) {

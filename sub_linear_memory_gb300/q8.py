@@ -55,7 +55,9 @@ for _name in ("codes_bytes", "scales_bytes", "rms_norm_bwd_workspace_bytes", "wg
 class Q8(NamedTuple):
     """An 8-bit matrix of ``cols`` columns.  codes: torch.float8_e4m3fn
     [rows, 128 * blocks]; scales: torch.uint8 [rows (or ceil(rows / 128)),
-    4 * ceil(blocks / 4)]; block_rows: 1, or 128 for a packed weight."""
+    4 * ceil(blocks / 4)]; block_rows: 1, or 128 for a packed weight.  Codes
+    made elsewhere: NaN codes stand only under scale 255 (``wgrad`` takes others
+    for 480)."""
 
     codes: torch.Tensor
     scales: torch.Tensor
