@@ -78,9 +78,10 @@ def empty(rows, cols, block_rows=1, device=None):
 
 
 def _stream(device):
-    binding.check_device(device)
-    # the stream's handle alone: torch.cuda.current_stream builds an object around it, for more
-    # than a small kernel's launch costs
+    # the device's number and the stream's handle alone: torch.cuda's functions around them cost
+    # more than a small kernel's launch
+    if device.index != torch._C._cuda_getDevice():
+        binding.check_device(device)
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 

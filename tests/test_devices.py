@@ -19,6 +19,7 @@ def test_tensors_elsewhere_are_refused(monkeypatch, module):
 
     stream = {"binding": binding, "q8": q8}[module]._stream
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     for device in ("cuda:1", "cpu"):
         with pytest.raises(ValueError, match="current CUDA device"):
             stream(torch.device(device))
