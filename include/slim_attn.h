@@ -448,6 +448,158 @@ slim_status slim_q8_wgrad(const void *dy, const void *x_codes, const void *x_sca
                           void *workspace, size_t workspace_bytes, int rows, int n, int k, slim_stream_t stream);
 size_t slim_q8_wgrad_workspace_bytes(int rows, int n, int k);
 
+/* ---- Linear attention with a decay for each head -----------------------------
+ *
+ * For every sequence, key-value head h with decay lambda = exp(log_decay[h]),
+ * and each of the `groups` query heads that share it (query head
+ * h * groups + g):
+ *       S_t = lambda S_(t-1) + k_t v_t^T   (dk x dv),   o_t = scale q_t^T S_t,
+ * i.e. o_t = scale sum_{j <= t} lambda^(t-j) (q_t . k_j) v_j, with no feature
+ * map and no normaliser.  Sequences are packed: rows [cu_seqlens[i],
+ * cu_seqlens[i + 1]) of the tensors, or with cu_seqlens NULL `seqs` sequences
+ * of tokens / seqs rows.  Rows outside every sequence are neither read nor
+ * written.  cu_seqlens (int32 on the device) has to ascend; entries outside
+ * [0, tokens] count as the nearest of the two.
+ *
+ * q, o: [tokens][heads * groups][dk or dv]; k, v: [tokens][heads][dk or dv];
+ * heads dense, rows `*_row` elements apart (so that q, k and v can be parts of
+ * one projection's rows); bf16, or fp32 with _f32.  log_decay: fp32 [heads], a
+ * constant of the model (it has no gradient); values above 0 count as 0, -inf
+ * is lambda = 0.  States: fp32 [places][heads][dk][dv].
+ *
+ * 1 <= dk, dv <= 256 and groups <= 64, else SLIM_ERR_UNSUPPORTED.  State and
+ * sums are fp32.  In bf16 a weighted score (q . k) lambda^n is rounded to bf16
+ * before its product with v where the tensor cores run, and so is the state
+ * before its product with q (2^-9 of each term, as the result's own rounding).
+ * A NaN or an infinity in a row also reaches earlier rows of its own sequence
+ * within 128 rows before it (0 times it is NaN), and no other sequence.
+ * Results depend on shape and lengths alone, not on timing.
+ *
+ * Tensors must not overlap, but for state_out = state_in.  workspace: device
+ * memory, 256-byte aligned, of slim_decay_workspace_bytes, used by one call at
+ * a time.  Every call only enqueues work on `stream` and allocates nothing. */
+typedef struct {
+  int tokens; /* rows of the tensors (of slim_decay_step: sequences) */
+  int seqs;   /* sequences (not used by slim_decay_step) */
+  int heads, groups, dk, dv;
+  int places; /* of the states; seqs (rows for slim_decay_step) where slots is NULL */
+  long long q_row, k_row, v_row, o_row; /* o_row: of o, or of its gradient */
+  long long dq_row, dk_row, dv_row;
+} slim_decay_shape;
+
+/* Bytes of workspace; equal: cu_seqlens will be NULL.  0 for an invalid shape. */
+size_t slim_decay_workspace_bytes(const slim_decay_shape *shape, int equal, int is_bwd);
+
+/* o, and the states behind the last rows.  state_in: the states before the
+ * first rows (NULL: zero).  state_out: NULL, or where the states go; it may be
+ * state_in.  slots: NULL (sequence i has place i), or int32 [seqs] on the
+ * device; a sequence whose slot is not in [0, places), or was named by an
+ * earlier one, starts from zero and leaves no state. */
+slim_status slim_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay, const int *cu_seqlens,
+                           const float *state_in, float *state_out, const int *slots, void *o,
+                           const slim_decay_shape *shape, float scale, void *workspace, size_t workspace_bytes,
+                           slim_stream_t stream);
+slim_status slim_decay_fwd_f32(const float *q, const float *k, const float *v, const float *log_decay,
+                               const int *cu_seqlens, const float *state_in, float *state_out, const int *slots,
+                               float *o, const slim_decay_shape *shape, float scale, void *workspace,
+                               size_t workspace_bytes, slim_stream_t stream);
+
+/* Gradients of sum(d_o . o) + sum(g_in . states behind the last rows): dq, dk,
+ * dv in the tensors' type, those of shared heads summed over their query
+ * heads, and g_out (or NULL), the gradient with respect to state_in.  g_in:
+ * NULL is zero.  g_out may be neither g_in nor state_in. */
+slim_status slim_decay_bwd(const void *q, const void *k, const void *v, const float *log_decay, const int *cu_seqlens,
+                           const void *d_o, const float *state_in, const float *g_in, float *g_out, void *dq, void *dk,
+                           void *dv, const slim_decay_shape *shape, float scale, void *workspace,
+                           size_t workspace_bytes, slim_stream_t stream);
+slim_status slim_decay_bwd_f32(const float *q, const float *k, const float *v, const float *log_decay,
+                               const int *cu_seqlens, const float *d_o, const float *state_in, const float *g_in,
+                               float *g_out, float *dq, float *dk, float *dv, const slim_decay_shape *shape,
+                               float scale, void *workspace, size_t workspace_bytes, slim_stream_t stream);
+
+/* One token of each of `tokens` sequences: its state takes the token's term in
+ * place, then o is read from it.  Row i has place slots[i] (slots NULL: i).  A
+ * row whose slot is not in [0, places), or was named by an earlier row, gets
+ * zeros and leaves every state as it was. */
+slim_status slim_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                            const int *slots, void *o, const slim_decay_shape *shape, float scale,
+                            slim_stream_t stream);
+slim_status slim_decay_step_f32(const float *q, const float *k, const float *v, const float *log_decay, float *state,
+                                const int *slots, float *o, const slim_decay_shape *shape, float scale,
+                                slim_stream_t stream);
+
+/* ---- Group norm of each row, with a gate --------------------------------------
+ *
+ * x [rows][cols] in `groups` groups of cols / groups consecutive columns:
+ *   n = (x - mean) * rstd, rstd = 1 / sqrt(var + eps), mean and (biased) var
+ *   over each group of each row,
+ *   y = n * gamma + beta, times silu(gate) = gate / (1 + e^-gate) where gate is
+ *   not NULL.
+ * x, gate, y: dense bf16, or fp32 with _f32; gamma, beta: fp32 [cols].  y may
+ * be neither x nor gate.  1 <= cols <= 16384, rows <= 2^30, else
+ * SLIM_ERR_INVALID_ARG or SLIM_ERR_UNSUPPORTED; cols a multiple of groups;
+ * eps >= 0.  Arithmetic is fp32, every result is rounded once. */
+slim_status slim_group_norm(const void *x, const float *gamma, const float *beta, const void *gate, float eps, void *y,
+                            int rows, int cols, int groups, slim_stream_t stream);
+slim_status slim_group_norm_f32(const float *x, const float *gamma, const float *beta, const float *gate, float eps,
+                                float *y, int rows, int cols, int groups, slim_stream_t stream);
+
+/* Its gradients.  dgate: where the gate's goes (NULL without a gate).  dgamma,
+ * dbeta: fp32 [cols], overwritten, summed in an order that depends on the
+ * shape alone; either may be NULL.  mean and rstd are formed again from x.
+ * Outputs may not be inputs.  workspace: 16-byte aligned device memory of
+ * slim_group_norm_bwd_workspace_bytes (needed for dgamma or dbeta only). */
+slim_status slim_group_norm_bwd(const void *dy, const void *x, const float *gamma, const float *beta, const void *gate,
+                                float eps, void *dx, void *dgate, float *dgamma, float *dbeta, void *workspace,
+                                size_t workspace_bytes, int rows, int cols, int groups, slim_stream_t stream);
+slim_status slim_group_norm_bwd_f32(const float *dy, const float *x, const float *gamma, const float *beta,
+                                    const float *gate, float eps, float *dx, float *dgate, float *dgamma, float *dbeta,
+                                    void *workspace, size_t workspace_bytes, int rows, int cols, int groups,
+                                    slim_stream_t stream);
+size_t slim_group_norm_bwd_workspace_bytes(int rows, int cols, int groups);
+
+/* ---- AdamW over many tensors ---------------------------------------------------
+ *
+ * For every element of every tensor that has a gradient, t = count[0] + 1:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = (1 - lr wd) p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * p is fp32, g bf16 (slim_adamw) or fp32 (slim_adamw_f32).  bits = 32: m and v
+ * are fp32.  bits = 8: m, and in the place of v its root r = sqrt(v), are 8-bit
+ * matrices of one row and n columns (see slim_q8_codes_bytes; zeros to begin
+ * with are codes 0 under scales 127).  Their values are rounded up or down at
+ * random with the probability of their place between two codes; element i of
+ * tensor k takes word i % 4 of Philox4x32-10 with counter
+ * (i / 4 mod 2^32, k, i / 2^34, t) and key (seed mod 2^32, seed div 2^32): its
+ * low 16 bits for m, its high 16 for r.  r > 0 is never rounded to 0.  A block
+ * with a value that is not finite is NaN from then on.
+ *
+ * count: int32 [2] on the device, (steps done, 0); the call adds 1 to the
+ * first, so that a captured step can be replayed.  Tensors without a gradient
+ * (grad NULL) or elements are left as they are.  No two tensors may overlap.
+ * 0 <= beta < 1, eps >= 0.  Every call only enqueues work on `stream` (one
+ * launch for each 496 tensors) and allocates nothing; `tensors` may be freed
+ * when it returns. */
+typedef struct {
+  float *param;
+  const void *grad;
+  void *m, *v;               /* fp32, or codes (16-byte aligned) */
+  void *m_scales, *v_scales; /* bits = 8 */
+  long long n;
+} slim_adamw_tensor;
+
+typedef struct {
+  float lr, beta1, beta2, eps, weight_decay;
+  int bits;
+  double log_beta1, log_beta2;   /* natural logarithms (-inf for beta = 0) */
+  unsigned long long seed;
+  const float *lr_device;        /* NULL, or where the kernel reads lr when it runs */
+} slim_adamw_options;
+
+slim_status slim_adamw(const slim_adamw_tensor *tensors, int n, const slim_adamw_options *options, int *count,
+                       slim_stream_t stream);
+slim_status slim_adamw_f32(const slim_adamw_tensor *tensors, int n, const slim_adamw_options *options, int *count,
+                           slim_stream_t stream);
+
 /* Bytes of workspace slim_attn_fwd (is_bwd = 0) or slim_attn_bwd (is_bwd = 1)
  * need for this shape on the current device (either I/O type).  0 for an
  * unsupported shape or an empty problem. */

@@ -113,6 +113,10 @@ EXPORTED = (
     "slim_q8_rms_norm_bwd_workspace_bytes", "slim_q8_gelu", "slim_q8_gelu_f32", "slim_q8_gelu_bwd",
     "slim_q8_gelu_bwd_f32", "slim_q8_matmul", "slim_q8_matmul_f32", "slim_q8_wgrad",
     "slim_q8_wgrad_workspace_bytes",
+    "slim_decay_fwd", "slim_decay_fwd_f32", "slim_decay_bwd", "slim_decay_bwd_f32", "slim_decay_step",
+    "slim_decay_step_f32", "slim_decay_workspace_bytes", "slim_group_norm", "slim_group_norm_f32",
+    "slim_group_norm_bwd", "slim_group_norm_bwd_f32", "slim_group_norm_bwd_workspace_bytes", "slim_adamw",
+    "slim_adamw_f32",
 )
 
 

@@ -9,9 +9,8 @@
 // block is cut at M columns.
 //
 // Gaussians come from Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel
-// random numbers: as easy as 1, 2, 3", SC 2011), written here from that
-// definition: counter (j, block, matrix, step mod 2^32), key (seed mod 2^32,
-// seed div 2^32); each 32-bit output x is the uniform (x + 1/2) / 2^32 and
+// random numbers: as easy as 1, 2, 3", SC 2011; philox.cuh): counter
+// (j, block, matrix, step mod 2^32), key (seed mod 2^32, seed div 2^32); each 32-bit output x is the uniform (x + 1/2) / 2^32 and
 // pairs of uniforms become two Gaussians by the Box-Muller transform.  Call j
 // of a block gives its Gaussians 4j .. 4j + 3; the first d^2 fill G row-major,
 // the next d^2 give the lengths (column c: the norm of g[d^2 + r d + c] over r).
@@ -27,29 +26,12 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "philox.cuh"
 
 namespace slim {
 namespace {
 
 constexpr int kOrfThreads = 256;
-
-__device__ __forceinline__ void philox4x32_10(uint32_t c[4], uint32_t k0, uint32_t k1) {
-  for (int r = 0; r < 10; ++r) {
-    if (r > 0) {
-      k0 += 0x9E3779B9u;
-      k1 += 0xBB67AE85u;
-    }
-    const uint64_t p0 = (uint64_t)0xD2511F53u * c[0];
-    const uint64_t p1 = (uint64_t)0xCD9E8D57u * c[2];
-    const uint32_t hi0 = (uint32_t)(p0 >> 32), lo0 = (uint32_t)p0;
-    const uint32_t hi1 = (uint32_t)(p1 >> 32), lo1 = (uint32_t)p1;
-    const uint32_t n0 = hi1 ^ c[1] ^ k0, n2 = hi0 ^ c[3] ^ k1;
-    c[0] = n0;
-    c[1] = lo1;
-    c[2] = n2;
-    c[3] = lo0;
-  }
-}
 
 // The four Gaussians 4j .. 4j + 3 of block b of matrix i (fp64): one Philox
 // call, two Box-Muller pairs.
