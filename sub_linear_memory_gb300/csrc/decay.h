@@ -87,6 +87,8 @@ cudaError_t prepare(const Prepare &p, cudaStream_t st);
 cudaError_t scan(const Scan &s, cudaStream_t st);
 template <typename T> cudaError_t mix_generic(const Launch &l, cudaStream_t st);
 int generic_tile(int dk, int dv);
+bool tc_supported(const Launch &l);
+cudaError_t mix_tc(const Launch &l, int *status, cudaStream_t st);
 
 // One token of each sequence.
 struct Step {

@@ -78,6 +78,11 @@ Cut generic_cut(const slim_decay_shape &s, bool equal) {
   return cut_tiles(s, equal, generic_tile(s.dk, s.dv), 2 * device_sms());
 }
 
+// On the tensor cores a block has an SM, and a tile takes a microsecond or so: shares of two tiles at least.
+Cut tc_cut(const slim_decay_shape &s, bool equal) { return cut_tiles(s, equal, 128, device_sms()); }
+
+bool tc_shape(const slim_decay_shape &s) { return s.dk == s.dv && (s.dk == 64 || s.dk == 128); }
+
 // The workspace's parts, in bytes from its start.
 struct Layout {
   size_t where, tiles, owner, place, totals[2], incoming[2], first, bytes;
@@ -110,7 +115,7 @@ struct Call {
   Layout at;
   const int *place;
   char *ws;
-  bool joined;
+  bool joined, tensor;
   template <typename T> T *part(size_t offset) const { return reinterpret_cast<T *>(ws + offset); }
 };
 
@@ -142,6 +147,14 @@ slim_status begin(const slim_decay_shape &s, const Cut &c, bool bwd, const int *
   return SLIM_OK;
 }
 
+// bf16 rows of the widths and alignment that they take go to the tensor cores (a training pass with 16 heads of 64
+// and 2 x 32768 rows: 1.8 ms, 8.8 on the CUDA cores), everything else to the CUDA cores.
+template <typename T> slim_status run_mix(const Launch &l, bool tensor, cudaStream_t st) {
+  if (!tensor) return finish(mix_generic<T>(l, st), st);
+  int *status = device_status_ptr();
+  return status ? finish(mix_tc(l, status, st), st) : SLIM_ERR_CUDA;
+}
+
 template <typename T>
 slim_status run_fwd(const void *q, const void *k, const void *v, const float *log_decay, const int *cu,
                     const float *state_in, float *state_out, const int *slots, void *o, const slim_decay_shape *shape,
@@ -163,27 +176,31 @@ slim_status run_fwd(const void *q, const void *k, const void *v, const float *lo
   }
   if (!aligned(log_decay, 4) || !aligned(cu, 4) || !aligned(slots, 4) || !aligned(state_in, 4) || !aligned(state_out, 4))
     return SLIM_ERR_UNSUPPORTED;
-  Call c;
-  SLIM_TRY(begin(s, generic_cut(s, !cu), false, cu, state_in || state_out ? slots : nullptr, workspace, workspace_bytes, st, c));
   Launch l{};
-  l.work = c.work;
   l.log_decay = log_decay;
   l.mixes = 1;
   Mix &m = l.mix[0];
   m = Mix{q, k, v, o, s.q_row, s.k_row, s.v_row, s.o_row, s.dk, s.dv, s.groups, 1, 0, scale, scale, 1.f, 0,
-          c.part<float>(c.at.incoming[0]), state_in && c.joined ? c.part<float>(c.at.first) : nullptr, state_in, state_out,
-          c.place, nullptr};
+          nullptr, nullptr, state_in, state_out, nullptr, nullptr};
+  Call c;
+  c.tensor = sizeof(T) == 2 && s.tokens && tc_supported(l);
+  SLIM_TRY(begin(s, c.tensor ? tc_cut(s, !cu) : generic_cut(s, !cu), false, cu, state_in || state_out ? slots : nullptr,
+                 workspace, workspace_bytes, st, c));
+  l.work = c.work;
+  m.place = c.place;
   if (c.joined) {
+    m.incoming = c.part<float>(c.at.incoming[0]);
+    m.first = state_in ? c.part<float>(c.at.first) : nullptr;
     Launch t = l;
     t.mix[0].totals = c.part<float>(c.at.totals[0]);
     t.mix[0].a_heads = 1;
-    SLIM_TRY(finish(mix_generic<T>(t, st), st));
+    SLIM_TRY(run_mix<T>(t, c.tensor, st));
     Scan sc{c.work, log_decay, s.dk * s.dv, {}, 1};
     sc.side[0] = {t.mix[0].totals, state_in, c.part<float>(c.at.incoming[0]), state_in ? c.part<float>(c.at.first) : nullptr,
                   c.place, 0};
     SLIM_TRY(finish(scan(sc, st), st));
   }
-  return finish(mix_generic<T>(l, st), st);
+  return run_mix<T>(l, c.tensor, st);
 }
 
 template <typename T>
@@ -213,32 +230,34 @@ slim_status run_bwd(const void *q, const void *k, const void *v, const float *lo
   }
   if (!aligned(log_decay, 4) || !aligned(cu, 4) || !aligned(state_in, 4) || !aligned(g_in, 4) || !aligned(g_out, 4))
     return SLIM_ERR_UNSUPPORTED;
-  Call c;
-  SLIM_TRY(begin(s, generic_cut(s, !cu), true, cu, nullptr, workspace, workspace_bytes, st, c));
-  const float *s_in = c.part<float>(c.at.incoming[0]), *gr_in = c.part<float>(c.at.incoming[1]);
   Launch l{};
-  l.work = c.work;
   l.log_decay = log_decay;
   l.mixes = 3;
   l.mix[0] = Mix{d_o, v, k, dq, s.o_row, s.v_row, s.k_row, s.dq_row, s.dv, s.dk, s.groups, 1, 0, scale, scale, 1.f, 1,
-                 s_in, nullptr, state_in, nullptr, nullptr, nullptr};
+                 nullptr, nullptr, state_in, nullptr, nullptr, nullptr};
   l.mix[1] = Mix{k, q, d_o, dv, s.k_row, s.q_row, s.o_row, s.dv_row, s.dk, s.dv, 1, s.groups, 1, scale, 1.f, scale, 0,
-                 gr_in, nullptr, g_in, g_out, nullptr, nullptr};
+                 nullptr, nullptr, g_in, g_out, nullptr, nullptr};
   l.mix[2] = Mix{v, d_o, q, dk, s.v_row, s.o_row, s.q_row, s.dk_row, s.dv, s.dk, 1, s.groups, 1, scale, 1.f, scale, 1,
-                 gr_in, nullptr, g_in, nullptr, nullptr, nullptr};
+                 nullptr, nullptr, g_in, nullptr, nullptr, nullptr};
+  Call c;
+  c.tensor = sizeof(T) == 2 && s.tokens && tc_supported(l);
+  SLIM_TRY(begin(s, c.tensor ? tc_cut(s, !cu) : generic_cut(s, !cu), true, cu, nullptr, workspace, workspace_bytes, st, c));
+  l.work = c.work;
   if (c.joined) {
+    l.mix[0].incoming = c.part<float>(c.at.incoming[0]);
+    l.mix[1].incoming = l.mix[2].incoming = c.part<float>(c.at.incoming[1]);
     Launch t = l;
     t.mixes = 2;
     t.mix[0] = Mix{nullptr, k, v, nullptr, 0, s.k_row, s.v_row, 0, s.dk, s.dv, 1, 1, 0, 0.f, 0.f, 1.f, 0,
                    nullptr, nullptr, nullptr, nullptr, nullptr, c.part<float>(c.at.totals[0])};
     t.mix[1].totals = c.part<float>(c.at.totals[1]);
-    SLIM_TRY(finish(mix_generic<T>(t, st), st));
+    SLIM_TRY(run_mix<T>(t, c.tensor, st));
     Scan sc{c.work, log_decay, s.dk * s.dv, {}, 2};
     sc.side[0] = {t.mix[0].totals, state_in, c.part<float>(c.at.incoming[0]), nullptr, nullptr, 0};
     sc.side[1] = {t.mix[1].totals, g_in, c.part<float>(c.at.incoming[1]), nullptr, nullptr, 1};
     SLIM_TRY(finish(scan(sc, st), st));
   }
-  return finish(mix_generic<T>(l, st), st);
+  return run_mix<T>(l, c.tensor, st);
 }
 
 template <typename T>
@@ -276,7 +295,8 @@ extern "C" {
 size_t slim_decay_workspace_bytes(const slim_decay_shape *shape, int equal, int is_bwd) {
   if (check_shape(shape) != SLIM_OK || shape->seqs == 0 || shape->heads == 0) return 0;
   if (equal && shape->tokens % shape->seqs) return 0;
-  return layout(*shape, generic_cut(*shape, equal != 0), is_bwd != 0).bytes;
+  const size_t bytes = layout(*shape, generic_cut(*shape, equal != 0), is_bwd != 0).bytes;
+  return tc_shape(*shape) ? std::max(bytes, layout(*shape, tc_cut(*shape, equal != 0), is_bwd != 0).bytes) : bytes;
 }
 
 slim_status slim_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay, const int *cu_seqlens,

@@ -1,0 +1,596 @@
+// decay_tc.cu -- linear attention with a decay on the tensor cores: bf16 rows, heads of 64 or
+// 128 columns.
+//
+// A block (one an SM) goes through its share of the tiles (decay.h), 128 rows
+// at a time, for one operator  out_i = sum lambda^(i-j) (a_i . b_j) c_j + lambda^(i+1) a_i X.
+// For each tile (and each query head of a group: a "unit") four products run
+// on tcgen05 with fp32 sums in tensor memory:
+//   scores   S = a b^T            128 x 128 x D
+//   read     R = a X              128 x D x D     (X: the state as bf16)
+//   within   W = (S . decay) c    128 x D x 128   (the weighted scores as bf16, from tensor memory)
+//   update   U = b~^T c           D x D x 128     (b~: the rows with their weight to the tile's end)
+// and out = read factor * R + within factor * W, state = lambda^n state + U.
+// The weights lambda^(i-j) are formed as products of two powers of at most 1,
+// so that nothing overflows however strong the decay.
+//
+// Roundings: out is rounded once; weighted scores and X are bf16 operands,
+// each off by 2^-9 of a term in the mean square, like the result itself.  The
+// state stays in fp32 registers, and b~ enters as two bf16 numbers (high part
+// and remainder, 2^-17), because states are results in fp32 too.
+//
+// Four roles: one warp loads tiles by TMA into a ring, one issues the MMAs,
+// and three warpgroups form the weighted scores, write the results, and keep
+// the state.  The bound is memory: 128 rows of four arrays take 2900 cycles of
+// this SM's share of HBM at D = 64 (5800 at 128), the products of a unit 1400
+// (2700).
+#include <cuda.h>
+
+#include "decay_common.cuh"
+#include "kernels.h"
+#include "q8_tc.cuh"
+#include "tma_host.h"
+
+namespace slim {
+namespace decay {
+namespace {
+
+using namespace tc;
+using q8::elect_lane;
+using q8::regs_dec;
+using q8::regs_inc;
+
+constexpr int kTile = 128, kThreads = 512;
+
+template <int D> struct Cfg {
+  static constexpr uint32_t kSlot = kTile * D * 2;     // a tile of one operand
+  static constexpr int kSlots = D == 64 ? 9 : 4;
+  static constexpr int kScores = D == 64 ? 2 : 1;      // buffers of scores
+  static constexpr uint32_t kWeighted = 2 * kSlot;     // b~: high parts and remainders
+  static constexpr uint32_t kState = D * D * 2;
+  static constexpr uint32_t kExchange = D == 64 ? 16384 : 0;
+  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kWeighted + kState + kExchange + 512;
+  // tensor memory columns
+  static constexpr uint32_t tScores = 0, tRead = 128 * kScores, tWithin = tRead + D, tUpdate = tWithin + D;
+};
+
+struct Args {
+  CUtensorMap maps[4];
+  Work work;
+  const float *log_decay;
+  int *status;
+  int mixes;
+  Mix mix[3];
+  signed char a[3], b[3], c[3];  // the operands' maps
+};
+
+// Zero-based phase counters of a ring or of a barrier.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ void next(int slots) {
+    if (++slot == (uint32_t)slots) slot = 0, phase ^= 1;
+  }
+};
+
+template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ Args p) {
+  using C = Cfg<D>;
+  extern __shared__ char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  char *generic = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t slots = base, weighted = slots + C::kSlots * C::kSlot, state = weighted + C::kWeighted,
+                 exchange = state + C::kState;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(generic + C::kSlots * C::kSlot + C::kWeighted + C::kState + C::kExchange);
+  uint64_t *full = bars, *empty = full + C::kSlots, *turned = empty + C::kSlots, *scored = turned + C::kSlots,
+           *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *known = added + 1, *drain = known + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
+  const int part = blockIdx.x / p.mixes, which = blockIdx.x - part * p.mixes;
+  const Mix &m = p.mix[which];
+  const Work &w = p.work;
+  const bool total = m.totals != nullptr, sums = m.b_heads > 1;
+  const int groups = max(m.a_heads, m.b_heads);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 2);   // the MMAs, the state's warpgroup
+      mbar_init(turned + i, 1);  // what the MMAs need of the state's warpgroup for these rows
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(scored + i, 1);
+      mbar_init(ready + i, 4);
+    }
+    mbar_init(done, 1);
+    mbar_init(taken, 4);
+    mbar_init(added, 1);
+    mbar_init(known, 1);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  if (warp == 0 && lane < 4) prefetch_tmap(p.maps + lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // A wait that has run out anywhere in the block lets every later one pass
+  // at once: the roles go through the rest of their loops, without loads and
+  // MMAs, so that none is missed at a barrier of its warpgroup.
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return !*abort && mbar_wait(bar, parity, p.status, abort);
+  };
+
+  Walk walk(w, part, m.rev);
+  Piece pc;
+  if (wg == 0) {
+    regs_dec<96>();
+    if (warp == 0) {
+      // ---- loads: b, a, c of each unit -------------------------------------------
+      const CUtensorMap *maps[3] = {p.maps + p.b[which], p.maps + (total ? 0 : p.a[which]), p.maps + p.c[which]};
+      const int b_heads = m.b_heads, a_heads = m.a_heads;
+      Ring r;
+      while (walk.next(w, pc)) {
+        if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
+        for (int k = 0; k < pc.t1 - pc.t0; ++k) {
+          const int row = pc.row0 + (m.rev ? pc.t1 - 1 - k : pc.t0 + k) * kTile;
+          for (int g = 0; g < groups; ++g) {
+            const int hb = pc.head * b_heads + (b_heads > 1 ? g : 0), ha = pc.head * a_heads + (a_heads > 1 ? g : 0);
+#pragma unroll
+            for (int o = 0; o < 3; ++o) {
+              if (o == 1 && total) continue;
+              const bool ok = __all_sync(0xffffffffu, wait(empty + r.slot, r.phase ^ 1));
+              if (ok && elect_lane()) {
+                mbar_arrive_expect_tx(full + r.slot, C::kSlot);
+                for (int x = 0; x < D / 64; ++x)
+                  tma_load_3d(generic + r.slot * C::kSlot + x * 16384, maps[o], full + r.slot, x * 64, o == 1 ? ha : hb, row);
+              }
+              __syncwarp();
+              r.next(C::kSlots);
+            }
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ---- MMAs ------------------------------------------------------------------
+      const uint32_t id_scores = make_idesc(128, 128, false, false), id_state = make_idesc(128, D, false, true),
+                     id_update = make_idesc(128, D, true, true);
+      Ring r;                    // the next unit whose scores are to be issued
+      uint32_t slot_a = 0, slot_b = 0, slot_c = 0, phase_c = 0;
+      uint32_t ahead[3] = {0, 0, 0}, ahead_phase[3] = {0, 0, 0};
+      bool alive = true;
+      uint32_t units_scored = 0, unit = 0, outs = 0, tiles = 0;
+      auto agree = [&](bool ok) { alive = alive && __all_sync(0xffffffffu, ok); return alive; };
+      // the slots of the unit at the ring's place
+      auto place = [&]() {
+        Ring t = r;
+        const int n = total ? 2 : 3;
+        for (int o = 0; o < n; ++o) {
+          const int at = total && o == 1 ? 2 : o;
+          ahead[at] = t.slot;
+          ahead_phase[at] = t.phase;
+          t.next(C::kSlots);
+        }
+        return t;
+      };
+      auto scores = [&]() {  // of unit `units_scored`, at `ahead`
+        if (alive && elect_lane()) {
+          const uint32_t a = slots + ahead[1] * C::kSlot, b = slots + ahead[0] * C::kSlot;
+          const uint32_t d = tmem + C::tScores + (units_scored % C::kScores) * 128;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) mma_bf16(d, desc_kmajor(a, kTile, 0, s), desc_kmajor(b, kTile, 0, s), id_scores, s > 0);
+          mma_commit(scored + units_scored % C::kScores);
+          mma_commit(empty + ahead[0]);
+        }
+        __syncwarp();
+        ++units_scored;
+      };
+      uint32_t held_a[2] = {0, 0}, held_c[2] = {0, 0}, held_cp[2] = {0, 0};  // slots of units whose scores are issued
+      while (walk.next(w, pc)) {
+        if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
+        for (int k = 0; k < pc.t1 - pc.t0; ++k, ++tiles) {
+          for (int g = 0; g < groups; ++g, ++unit) {
+            const bool last = g == groups - 1, update = sums || last;
+            if (total) {
+              const Ring after = place();
+              slot_b = ahead[0], slot_c = ahead[2], phase_c = ahead_phase[2];
+              r = after;
+              agree(wait(full + slot_b, ahead_phase[0]));
+              agree(wait(full + slot_c, phase_c));
+            } else {
+              // scores of this unit, if they are not under way
+              if (units_scored == unit) {
+                const Ring after = place();
+                agree(wait(full + ahead[0], ahead_phase[0]));
+                agree(wait(full + ahead[1], ahead_phase[1]));
+                held_a[unit & 1] = ahead[1], held_c[unit & 1] = ahead[2], held_cp[unit & 1] = ahead_phase[2];
+                scores();
+                r = after;
+              }
+              slot_a = held_a[unit & 1], slot_c = held_c[unit & 1], phase_c = held_cp[unit & 1];
+              agree(wait(full + slot_c, phase_c));
+              // and those of the next one, if its rows are here: whether there is a next one shows in the
+              // barrier alone, which completes no phase without a load
+              if (C::kScores == 2 && units_scored == unit + 1) {
+                const Ring after = place();
+                const bool here = __shfl_sync(0xffffffffu, (int)(mbar_test(full + ahead[0], ahead_phase[0]) &&
+                                                                 mbar_test(full + ahead[1], ahead_phase[1])), 0);
+                if (here && alive) {
+                  held_a[(unit + 1) & 1] = ahead[1], held_c[(unit + 1) & 1] = ahead[2], held_cp[(unit + 1) & 1] = ahead_phase[2];
+                  scores();
+                  r = after;
+                }
+              }
+              const uint32_t a = slots + slot_a * C::kSlot;
+              if (g == 0) agree(wait(known, tiles & 1));
+              if (g == 0 || !sums) {
+                agree(wait(taken, (outs & 1) ^ 1));
+                if (alive && elect_lane()) {
+                  tc_fence_after();
+#pragma unroll
+                  for (int s = 0; s < D / 16; ++s)
+                    mma_bf16(tmem + C::tRead, desc_kmajor(a, kTile, 0, s), desc_mnmajor(state, D, 0, s), id_state, s > 0);
+                }
+                __syncwarp();
+              }
+            }
+            agree(wait(turned + slot_c, phase_c));
+            const uint32_t c = slots + slot_c * C::kSlot;
+            if (update) {
+              if (alive && elect_lane()) {
+                tc_fence_after();
+                const bool first = !sums || g == 0;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                  mma_bf16(tmem + C::tUpdate, desc_mnmajor(weighted, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update,
+                           s > 0 || !first);
+                if constexpr (D == 128) {
+#pragma unroll
+                  for (int s = 0; s < 8; ++s)
+                    mma_bf16(tmem + C::tUpdate, desc_mnmajor(weighted + C::kSlot, kTile, 0, s), desc_mnmajor(c, kTile, 0, s),
+                             id_update, 1);
+                }
+                mma_commit(added);
+                if (total) {
+                  mma_commit(empty + slot_b);
+                  mma_commit(empty + slot_c);
+                }
+              }
+              __syncwarp();
+            }
+            if (!total) {
+              const uint32_t sb = unit % C::kScores;
+              agree(wait(ready + sb, (unit / C::kScores) & 1));
+              if (alive && elect_lane()) {
+                tc_fence_after();
+                const bool first = !sums || g == 0;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                  mma_bf16_ta(tmem + C::tWithin, tmem + C::tScores + sb * 128 + s * 8, desc_mnmajor(c, kTile, 0, s), id_state,
+                              s > 0 || !first);
+                mma_commit(empty + slot_a);
+                mma_commit(empty + slot_c);
+                if (last || !sums) mma_commit(done);
+              }
+              __syncwarp();
+              if (last || !sums) ++outs;
+            }
+          }
+        }
+      }
+      // what was issued has to end before its tensor memory goes
+      if (elect_lane()) {
+        mma_commit(drain);
+        mbar_drain(drain, 0);
+      }
+      __syncwarp();
+    }
+  } else if (wg == 1) {
+    // ---- weighted scores: thread t has row t -------------------------------------
+    const int t = threadIdx.x - 128, q = t >> 5;
+    const uint32_t row_base = tmem_addr(tmem, q * 32, C::tScores);
+    uint32_t unit = 0;
+    while (walk.next(w, pc)) {
+      if (total || pc.rows == 0) continue;
+      const float g2 = log2_decay(p.log_decay, pc.head);
+      float col[32];  // lambda^(distance to the block's nearer end)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) col[j] = exp2f(g2 * (float)(m.rev ? j : 31 - j));
+      for (int k = 0; k < pc.t1 - pc.t0; ++k) {
+        const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
+        for (int g = 0; g < groups; ++g, ++unit) {
+          const uint32_t sb = unit % C::kScores, at = row_base + sb * 128;
+          wait(scored + sb, (unit / C::kScores) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int jb = 0; jb < 4; ++jb) {
+            float v[32];
+            const bool diagonal = jb == q, live = m.rev ? jb > q : jb < q;
+            if (diagonal || live) {
+              tmem_ld32(at + jb * 32, v);
+              const int c0 = jb * 32;
+              if (live) {
+                const float away = exp2f(g2 * (float)(m.rev ? c0 - t : t - c0 - 31));
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= col[j] * away;
+                if (m.rev && c0 + 32 > n) {
+                  // chosen, not multiplied with 0: the rows behind the sequence may hold anything
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) v[j] = c0 + j < n ? v[j] : 0.f;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const int apart = m.rev ? j - lane : lane - j;
+                  const float d = exp2f(g2 * (float)apart);
+                  v[j] = apart >= 0 && (!m.rev || c0 + j < n) ? v[j] * d : 0.f;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+            // two numbers to a column: block jb's 16 columns lie where scores of blocks already read were
+            float packed[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) packed[j] = __uint_as_float(pack_bf16(v[2 * j], v[2 * j + 1]));
+            tmem_st16(at + jb * 16, packed);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + sb);
+        }
+      }
+    }
+  } else if (wg == 2) {
+    // ---- results: thread t has row t ---------------------------------------------
+    regs_dec<80>();
+    const int t = threadIdx.x - 256, q = t >> 5;
+    const uint32_t row_base = tmem_addr(tmem, q * 32, 0);
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(m.out);
+    uint32_t outs = 0;
+    while (walk.next(w, pc)) {
+      if (total || pc.rows == 0) continue;
+      const float g2 = log2_decay(p.log_decay, pc.head);
+      for (int k = 0; k < pc.t1 - pc.t0; ++k) {
+        const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
+        const float read = m.read * exp2f(g2 * (float)(m.rev ? n - 1 - t : t + 1));  // rows past n are not written
+        for (int g = 0; g < (sums ? 1 : groups); ++g, ++outs) {
+          wait(done, outs & 1);
+          tc_fence_after();
+          __nv_bfloat16 *dst = out + ((long long)pc.row0 + tile * kTile + t) * m.out_row + (long long)(pc.head * m.a_heads + g) * D;
+#pragma unroll
+          for (int x = 0; x < D; x += 16) {
+            float r[16], v[16];
+            tmem_ld16x2(row_base + C::tRead + x, row_base + C::tWithin + x, r, v);
+            uint32_t u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              u[j] = pack_bf16(fmaf(r[2 * j], read, m.within * v[2 * j]), fmaf(r[2 * j + 1], read, m.within * v[2 * j + 1]));
+            if (t < n) {
+              *reinterpret_cast<uint4 *>(dst + x) = make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(taken);
+        }
+      }
+    }
+  } else {
+    // ---- the state -----------------------------------------------------------------
+    // Thread t weighs row t of b.  Of the state it has row t (D = 128), or
+    // half of row t % 64: with D = 64 the update's rows 0-63 are those of the
+    // high parts and 64-127 those of the remainders, so two threads exchange
+    // halves and add.
+    regs_inc<208>();
+    constexpr int kOwn = D == 64 ? 32 : 128;
+    const int t = threadIdx.x - 384, q = t >> 5;
+    const int srow = D == 64 ? t & 63 : t, scol = D == 64 ? (t >> 6) * 32 : 0;
+    const uint32_t row_base = tmem_addr(tmem, q * 32, C::tUpdate);
+    constexpr int kBar = 1;
+    float s[kOwn];
+    Ring r;
+    uint32_t unit = 0, adds = 0;
+    auto publish = [&]() {  // the state as the operand [x][y]
+#pragma unroll
+      for (int i = 0; i < kOwn; i += 8) st_bf16x8(state + sw128_offset(srow, scol + i, D), s + i);
+      fence_async_smem();
+      tc_fence_before();
+      named_barrier_sync(kBar, 128);
+      if (t == 0) mbar_arrive(known);
+    };
+    while (walk.next(w, pc)) {
+      if (total && !piece_has_total(m, pc)) continue;
+      const float g2 = log2_decay(p.log_decay, pc.head);
+      const float *start = piece_start(w, m, pc, part);
+      // in memory [x][y], or transposed: step by step either way from one address
+      const int first = m.transposed ? scol * D + srow : srow * D + scol;
+      if (!start) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) s[i] = 0.f;
+      } else if (m.transposed) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) s[i] = start[first + i * D];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) s[i] = start[first + i];
+      }
+      const int count = pc.rows == 0 ? 0 : pc.t1 - pc.t0;
+      if (!total && count) publish();
+      for (int k = 0; k < count; ++k) {
+        const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
+        const float weight = m.add * exp2f(g2 * (float)(m.rev ? t + 1 : n - 1 - t));
+        for (int g = 0; g < groups; ++g, ++unit) {
+          const bool update = sums || g == groups - 1;
+          uint32_t at[3] = {0, 0, 0};
+#pragma unroll
+          for (int o = 0; o < 3; ++o) {
+            if (o == 1 && total) continue;
+            wait(full + r.slot, r.phase);
+            at[o] = r.slot;
+            r.next(C::kSlots);
+          }
+          const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
+          if (update) {
+#pragma unroll 4
+            for (int x = 0; x < D; x += 8) {
+              float v[8], lo[8];
+              const uint32_t off = sw128_offset(t, x, kTile);
+              if (t < n) {
+                ld_bf16x8(b + off, v);
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float v0 = v[2 * j] * weight, v1 = v[2 * j + 1] * weight;
+                  h[j] = pack_bf16(v0, v1);
+                  lo[2 * j] = v0 - __uint_as_float(h[j] << 16);
+                  lo[2 * j + 1] = v1 - __uint_as_float(h[j] & 0xffff0000u);
+                }
+                st_shared_v4(weighted + off, h[0], h[1], h[2], h[3]);
+                st_bf16x8(weighted + C::kSlot + off, lo);
+              } else {
+                st_shared_v4(weighted + off, 0, 0, 0, 0);
+                st_shared_v4(weighted + C::kSlot + off, 0, 0, 0, 0);
+              }
+            }
+          }
+          if (t >= n) {
+            // rows behind the sequence: 0 times whatever they hold has to be 0
+#pragma unroll
+            for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+          }
+          fence_async_smem();
+          named_barrier_sync(kBar, 128);
+          if (t == 0) {
+#pragma unroll
+            for (int o = 0; o < 3; ++o) {
+              if (o == 1 && total) continue;
+              mbar_arrive(turned + at[o]);  // every slot's, so that its phases go with the loads'
+              mbar_arrive(empty + at[o]);
+            }
+          }
+          if (!update) continue;
+          wait(added, adds & 1);
+          ++adds;
+          if (g < groups - 1) continue;
+          tc_fence_after();
+          const float keep = exp2f(g2 * (float)n);
+          if constexpr (D == 64) {
+            float u[32], v[32];
+            tmem_ld32x2(row_base, row_base + 32, u, v);
+            const bool low = t >= 64;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float *give = low ? u + 4 * i : v + 4 * i;
+              st_shared_v4(exchange + (i * 128 + t) * 16, __float_as_uint(give[0]), __float_as_uint(give[1]),
+                           __float_as_uint(give[2]), __float_as_uint(give[3]));
+            }
+            named_barrier_sync(kBar, 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x[4];
+              ld_shared_v4f(exchange + (i * 128 + (t ^ 64)) * 16, x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[4 * i + j] = fmaf(s[4 * i + j], keep, (low ? v[4 * i + j] : u[4 * i + j]) + x[j]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < D; x += 16) {
+              float u[16];
+              tmem_ld16(row_base + x, u);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) s[x + j] = fmaf(s[x + j], keep, u[j]);
+            }
+          }
+          tc_fence_before();
+          if (!total && k < count - 1) publish();
+        }
+      }
+      float *end = piece_end(w, m, pc, part);
+      if (end && m.transposed) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) end[first + i * D] = s[i];
+      } else if (end) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) end[first + i] = s[i];
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort && threadIdx.x == 0)  // copies still on their way land before the block leaves
+    for (int i = 0; i < C::kSlots; ++i)
+      for (uint32_t parity = 0; parity < 2; ++parity) mbar_drain(full + i, parity, 20000000ull);
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D> cudaError_t launch(const Args &a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  tc_kernel<D><<<a.work.parts * a.mixes, kThreads, Cfg<D>::kBytes, st>>>(a);
+  return cudaGetLastError();
+}
+
+// [tokens][heads][D], rows `row` elements apart; boxes of 128 rows and 64 columns of one head.
+bool make_map(CUtensorMap *map, const void *p, int tokens, long long heads, int d, long long row) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)row * 2};
+  const cuuint32_t box[3] = {64, 1, kTile};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Heads of 64 or 128 columns whose rows start on 16 bytes, as TMA and 16-byte stores want them.
+bool tc_supported(const Launch &l) {
+  for (int i = 0; i < l.mixes; ++i) {
+    const Mix &m = l.mix[i];
+    if (m.x != m.y || (m.x != 64 && m.x != 128)) return false;
+    const void *ptrs[4] = {m.a, m.b, m.c, m.out};
+    const long long rows[4] = {m.a_row, m.b_row, m.c_row, m.out_row};
+    for (int k = 0; k < 4; ++k)
+      if ((reinterpret_cast<uintptr_t>(ptrs[k]) & 15) || rows[k] % 8 || rows[k] >= (1ll << 38)) return false;
+  }
+  return true;
+}
+
+cudaError_t mix_tc(const Launch &l, int *status, cudaStream_t st) {
+  ProfScope ps(l.mix[0].totals ? "decay_totals" : "decay_mix", st);
+  Args a{};
+  a.work = l.work;
+  a.log_decay = l.log_decay;
+  a.status = status;
+  a.mixes = l.mixes;
+  int used = 0;
+  struct { const void *p; int heads; long long row; } seen[4] = {};
+  auto map_of = [&](const void *p, int heads, long long row, int d) -> int {
+    for (int i = 0; i < used; ++i)
+      if (seen[i].p == p && seen[i].heads == heads && seen[i].row == row) return i;
+    if (used == 4 || !make_map(a.maps + used, p, l.work.tokens, (long long)heads * l.work.heads, d, row)) return -1;
+    seen[used] = {p, heads, row};
+    return used++;
+  };
+  for (int i = 0; i < l.mixes; ++i) {
+    const Mix &m = a.mix[i] = l.mix[i];
+    a.a[i] = (signed char)(m.totals ? 0 : map_of(m.a, m.a_heads, m.a_row, m.x));
+    a.b[i] = (signed char)map_of(m.b, m.b_heads, m.b_row, m.x);
+    a.c[i] = (signed char)map_of(m.c, m.b_heads, m.c_row, m.x);
+    if (a.a[i] < 0 || a.b[i] < 0 || a.c[i] < 0) return cudaErrorInvalidValue;
+  }
+  for (int i = used; i < 4; ++i) a.maps[i] = a.maps[0];
+  return l.mix[0].x == 64 ? launch<64>(a, st) : launch<128>(a, st);
+}
+
+}  // namespace decay
+}  // namespace slim
