@@ -305,7 +305,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           const uint32_t sb = unit % C::kScores, at = row_base + sb * 128;
           wait(scored + sb, (unit / C::kScores) & 1);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int jb = 0; jb < 4; ++jb) {
             float v[32];
             const bool diagonal = jb == q, live = m.rev ? jb > q : jb < q;
@@ -313,7 +313,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
               tmem_ld32(at + jb * 32, v);
               const int c0 = jb * 32;
               if (live) {
-                const float away = exp2f(g2 * (float)(m.rev ? c0 - t : t - c0 - 31));
+                const float away = ex2_ftz(g2 * (float)(m.rev ? c0 - t : t - c0 - 31));
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] *= col[j] * away;
                 if (m.rev && c0 + 32 > n) {
@@ -325,7 +325,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                   const int apart = m.rev ? j - lane : lane - j;
-                  const float d = exp2f(g2 * (float)apart);
+                  const float d = ex2_ftz(g2 * (float)apart);
                   v[j] = apart >= 0 && (!m.rev || c0 + j < n) ? v[j] * d : 0.f;
                 }
               }
@@ -363,7 +363,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           wait(done, outs & 1);
           tc_fence_after();
           __nv_bfloat16 *dst = out + ((long long)pc.row0 + tile * kTile + t) * m.out_row + (long long)(pc.head * m.a_heads + g) * D;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < D; x += 16) {
             float r[16], v[16];
             tmem_ld16x2(row_base + C::tRead + x, row_base + C::tWithin + x, r, v);
@@ -438,7 +438,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           }
           const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
           if (update) {
-#pragma unroll 4
+#pragma unroll 1
             for (int x = 0; x < D; x += 8) {
               float v[8], lo[8];
               const uint32_t off = sw128_offset(t, x, kTile);
@@ -462,7 +462,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           }
           if (t >= n) {
             // rows behind the sequence: 0 times whatever they hold has to be 0
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
           }
           fence_async_smem();
