@@ -43,14 +43,15 @@ constexpr int kTile = 128, kThreads = 512;
 
 template <int D> struct Cfg {
   static constexpr uint32_t kSlot = kTile * D * 2;     // a tile of one operand
-  static constexpr int kSlots = D == 64 ? 9 : 4;
-  static constexpr int kScores = D == 64 ? 2 : 1;      // buffers of scores
+  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kBuffers = D == 64 ? 2 : 1;     // of scores, b~, X and updates
   static constexpr uint32_t kWeighted = 2 * kSlot;     // b~: high parts and remainders
   static constexpr uint32_t kState = D * D * 2;
   static constexpr uint32_t kExchange = D == 64 ? 16384 : 0;
-  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kWeighted + kState + kExchange + 512;
+  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kBuffers * (kWeighted + kState) + kExchange + 512;
   // tensor memory columns
-  static constexpr uint32_t tScores = 0, tRead = 128 * kScores, tWithin = tRead + D, tUpdate = tWithin + D;
+  static constexpr uint32_t tScores = 0, tRead = 128 * kBuffers, tWithin = tRead + D, tUpdate = tWithin + D;
+  static_assert(tUpdate + kBuffers * D <= 512, "tensor memory");
 };
 
 struct Args {
@@ -76,11 +77,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
   extern __shared__ char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   char *generic = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t slots = base, weighted = slots + C::kSlots * C::kSlot, state = weighted + C::kWeighted,
-                 exchange = state + C::kState;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(generic + C::kSlots * C::kSlot + C::kWeighted + C::kState + C::kExchange);
+  const uint32_t slots = base, weighted = slots + C::kSlots * C::kSlot, state = weighted + C::kBuffers * C::kWeighted,
+                 exchange = state + C::kBuffers * C::kState;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(generic + (exchange - base) + C::kExchange);
   uint64_t *full = bars, *empty = full + C::kSlots, *turned = empty + C::kSlots, *scored = turned + C::kSlots,
-           *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *known = added + 1, *drain = known + 1;
+           *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *known = added + 2, *drain = known + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -100,11 +101,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     for (int i = 0; i < 2; ++i) {
       mbar_init(scored + i, 1);
       mbar_init(ready + i, 4);
+      mbar_init(added + i, 1);
+      mbar_init(known + i, 1);
     }
     mbar_init(done, 1);
     mbar_init(taken, 4);
-    mbar_init(added, 1);
-    mbar_init(known, 1);
     mbar_init(drain, 1);
     *abort = 0;
     fence_barrier_init();
@@ -161,7 +162,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       uint32_t slot_a = 0, slot_b = 0, slot_c = 0, phase_c = 0;
       uint32_t ahead[3] = {0, 0, 0}, ahead_phase[3] = {0, 0, 0};
       bool alive = true;
-      uint32_t units_scored = 0, unit = 0, outs = 0, tiles = 0;
+      uint32_t units_scored = 0, unit = 0, outs = 0, tiles = 0, updates = 0;
       auto agree = [&](bool ok) { alive = alive && __all_sync(0xffffffffu, ok); return alive; };
       // the slots of the unit at the ring's place
       auto place = [&]() {
@@ -178,11 +179,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       auto scores = [&]() {  // of unit `units_scored`, at `ahead`
         if (alive && elect_lane()) {
           const uint32_t a = slots + ahead[1] * C::kSlot, b = slots + ahead[0] * C::kSlot;
-          const uint32_t d = tmem + C::tScores + (units_scored % C::kScores) * 128;
+          const uint32_t d = tmem + C::tScores + (units_scored % C::kBuffers) * 128;
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) mma_bf16(d, desc_kmajor(a, kTile, 0, s), desc_kmajor(b, kTile, 0, s), id_scores, s > 0);
-          mma_commit(scored + units_scored % C::kScores);
+          mma_commit(scored + units_scored % C::kBuffers);
           mma_commit(empty + ahead[0]);
         }
         __syncwarp();
@@ -194,6 +195,19 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         for (int k = 0; k < pc.t1 - pc.t0; ++k, ++tiles) {
           for (int g = 0; g < groups; ++g, ++unit) {
             const bool last = g == groups - 1, update = sums || last;
+            auto read = [&]() {
+              if (g == 0) agree(wait(known + tiles % C::kBuffers, (tiles / C::kBuffers) & 1));
+              if (g > 0 && sums) return;
+              agree(wait(taken, (outs & 1) ^ 1));
+              if (alive && elect_lane()) {
+                tc_fence_after();
+                const uint32_t a = slots + slot_a * C::kSlot, x = state + (tiles % C::kBuffers) * C::kState;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                  mma_bf16(tmem + C::tRead, desc_kmajor(a, kTile, 0, s), desc_mnmajor(x, D, 0, s), id_state, s > 0);
+              }
+              __syncwarp();
+            };
             if (total) {
               const Ring after = place();
               slot_b = ahead[0], slot_c = ahead[2], phase_c = ahead_phase[2];
@@ -214,7 +228,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
               agree(wait(full + slot_c, phase_c));
               // and those of the next one, if its rows are here: whether there is a next one shows in the
               // barrier alone, which completes no phase without a load
-              if (C::kScores == 2 && units_scored == unit + 1) {
+              if (C::kBuffers == 2 && units_scored == unit + 1) {
                 const Ring after = place();
                 const bool here = __shfl_sync(0xffffffffu, (int)(mbar_test(full + ahead[0], ahead_phase[0]) &&
                                                                  mbar_test(full + ahead[1], ahead_phase[1])), 0);
@@ -224,46 +238,38 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                   r = after;
                 }
               }
-              const uint32_t a = slots + slot_a * C::kSlot;
-              if (g == 0) agree(wait(known, tiles & 1));
-              if (g == 0 || !sums) {
-                agree(wait(taken, (outs & 1) ^ 1));
-                if (alive && elect_lane()) {
-                  tc_fence_after();
-#pragma unroll
-                  for (int s = 0; s < D / 16; ++s)
-                    mma_bf16(tmem + C::tRead, desc_kmajor(a, kTile, 0, s), desc_mnmajor(state, D, 0, s), id_state, s > 0);
-                }
-                __syncwarp();
-              }
             }
+            // with two buffers the update goes first, ahead of the state that this tile reads; with one it would
+            // overwrite what the state's warpgroup has yet to take
+            if (C::kBuffers == 1 && !total) read();
             agree(wait(turned + slot_c, phase_c));
             const uint32_t c = slots + slot_c * C::kSlot;
             if (update) {
               if (alive && elect_lane()) {
                 tc_fence_after();
                 const bool first = !sums || g == 0;
+                const uint32_t d = tmem + C::tUpdate + (tiles % C::kBuffers) * D, b = weighted + (updates % C::kBuffers) * C::kWeighted;
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  mma_bf16(tmem + C::tUpdate, desc_mnmajor(weighted, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update,
-                           s > 0 || !first);
+                  mma_bf16(d, desc_mnmajor(b, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update, s > 0 || !first);
                 if constexpr (D == 128) {
 #pragma unroll
                   for (int s = 0; s < 8; ++s)
-                    mma_bf16(tmem + C::tUpdate, desc_mnmajor(weighted + C::kSlot, kTile, 0, s), desc_mnmajor(c, kTile, 0, s),
-                             id_update, 1);
+                    mma_bf16(d, desc_mnmajor(b + C::kSlot, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update, 1);
                 }
-                mma_commit(added);
+                mma_commit(added + updates % C::kBuffers);
                 if (total) {
                   mma_commit(empty + slot_b);
                   mma_commit(empty + slot_c);
                 }
               }
               __syncwarp();
+              ++updates;
             }
+            if (C::kBuffers == 2 && !total) read();
             if (!total) {
-              const uint32_t sb = unit % C::kScores;
-              agree(wait(ready + sb, (unit / C::kScores) & 1));
+              const uint32_t sb = unit % C::kBuffers;
+              agree(wait(ready + sb, (unit / C::kBuffers) & 1));
               if (alive && elect_lane()) {
                 tc_fence_after();
                 const bool first = !sums || g == 0;
@@ -296,38 +302,46 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     while (walk.next(w, pc)) {
       if (total || pc.rows == 0) continue;
       const float g2 = log2_decay(p.log_decay, pc.head);
-      float col[32];  // lambda^(distance to the block's nearer end)
+      // Powers of lambda: from a column to the block's end that is nearer the rows, and on the diagonal block.
+      float2 col[16], diag[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) col[j] = exp2f(g2 * (float)(m.rev ? j : 31 - j));
+      for (int j = 0; j < 16; ++j) {
+        const int j0 = 2 * j, j1 = 2 * j + 1;
+        col[j] = make_float2(exp2f(g2 * (float)(m.rev ? j0 : 31 - j0)), exp2f(g2 * (float)(m.rev ? j1 : 31 - j1)));
+        diag[j] = make_float2(exp2f(g2 * fmaxf(0.f, (float)(m.rev ? j0 - lane : lane - j0))),
+                              exp2f(g2 * fmaxf(0.f, (float)(m.rev ? j1 - lane : lane - j1))));
+      }
       for (int k = 0; k < pc.t1 - pc.t0; ++k) {
         const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
         for (int g = 0; g < groups; ++g, ++unit) {
-          const uint32_t sb = unit % C::kScores, at = row_base + sb * 128;
-          wait(scored + sb, (unit / C::kScores) & 1);
+          const uint32_t sb = unit % C::kBuffers, at = row_base + sb * 128;
+          wait(scored + sb, (unit / C::kBuffers) & 1);
           tc_fence_after();
 #pragma unroll 1
           for (int jb = 0; jb < 4; ++jb) {
             float v[32];
             const bool diagonal = jb == q, live = m.rev ? jb > q : jb < q;
+            const int c0 = jb * 32;
             if (diagonal || live) {
-              tmem_ld32(at + jb * 32, v);
-              const int c0 = jb * 32;
+              tmem_ld32(at + c0, v);
               if (live) {
                 const float away = ex2_ftz(g2 * (float)(m.rev ? c0 - t : t - c0 - 31));
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= col[j] * away;
-                if (m.rev && c0 + 32 > n) {
-                  // chosen, not multiplied with 0: the rows behind the sequence may hold anything
-#pragma unroll
-                  for (int j = 0; j < 32; ++j) v[j] = c0 + j < n ? v[j] : 0.f;
+                for (int j = 0; j < 16; ++j) {
+                  const float2 x = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), __fmul2_rn(col[j], make_float2(away, away)));
+                  v[2 * j] = x.x, v[2 * j + 1] = x.y;
                 }
               } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                  const int apart = m.rev ? j - lane : lane - j;
-                  const float d = ex2_ftz(g2 * (float)apart);
-                  v[j] = apart >= 0 && (!m.rev || c0 + j < n) ? v[j] * d : 0.f;
+                  const float d = j & 1 ? diag[j / 2].y : diag[j / 2].x;
+                  v[j] = (m.rev ? j >= lane : j <= lane) ? v[j] * d : 0.f;
                 }
+              }
+              if (m.rev && c0 + 32 > n) {
+                // chosen, not multiplied with 0: the rows behind the sequence may hold anything
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = c0 + j < n ? v[j] : 0.f;
               }
             } else {
 #pragma unroll
@@ -396,14 +410,52 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     constexpr int kBar = 1;
     float s[kOwn];
     Ring r;
-    uint32_t unit = 0, adds = 0;
+    uint32_t adds = 0, updates = 0, tiles = 0;  // updates waited for, handed out; tiles whose state is published
     auto publish = [&]() {  // the state as the operand [x][y]
+      const uint32_t buffer = tiles++ % C::kBuffers, x = state + buffer * C::kState;
 #pragma unroll
-      for (int i = 0; i < kOwn; i += 8) st_bf16x8(state + sw128_offset(srow, scol + i, D), s + i);
+      for (int i = 0; i < kOwn; i += 8) st_bf16x8(x + sw128_offset(srow, scol + i, D), s + i);
       fence_async_smem();
-      tc_fence_before();
       named_barrier_sync(kBar, 128);
-      if (t == 0) mbar_arrive(known);
+      if (t == 0) mbar_arrive(known + buffer);
+    };
+    uint32_t summed = 0;  // tiles whose update is in the state
+    // Waits for the oldest update handed out; where it is its tile's last, the state takes the tile's sum.
+    auto take = [&](bool whole, float keep) {
+      wait(added + adds % C::kBuffers, (adds / C::kBuffers) & 1);
+      ++adds;
+      if (!whole) return;
+      tc_fence_after();
+      const uint32_t from = row_base + (summed % C::kBuffers) * D;
+      ++summed;
+      if constexpr (D == 64) {
+        float u[32], v[32];
+        tmem_ld32x2(from, from + 32, u, v);
+        const bool low = t >= 64;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float *give = low ? u + 4 * i : v + 4 * i;
+          st_shared_v4(exchange + (i * 128 + t) * 16, __float_as_uint(give[0]), __float_as_uint(give[1]),
+                       __float_as_uint(give[2]), __float_as_uint(give[3]));
+        }
+        named_barrier_sync(kBar, 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x[4];
+          ld_shared_v4f(exchange + (i * 128 + (t ^ 64)) * 16, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[4 * i + j] = fmaf(s[4 * i + j], keep, (low ? v[4 * i + j] : u[4 * i + j]) + x[j]);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < D; x += 16) {
+          float u[16];
+          tmem_ld16(from + x, u);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[x + j] = fmaf(s[x + j], keep, u[j]);
+        }
+      }
+      tc_fence_before();
     };
     while (walk.next(w, pc)) {
       if (total && !piece_has_total(m, pc)) continue;
@@ -422,11 +474,13 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         for (int i = 0; i < kOwn; ++i) s[i] = start[first + i];
       }
       const int count = pc.rows == 0 ? 0 : pc.t1 - pc.t0;
+      bool pending_whole = false;
+      float pending_keep = 0.f;
       if (!total && count) publish();
       for (int k = 0; k < count; ++k) {
         const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
-        const float weight = m.add * exp2f(g2 * (float)(m.rev ? t + 1 : n - 1 - t));
-        for (int g = 0; g < groups; ++g, ++unit) {
+        const float keep = exp2f(g2 * (float)n), weight = m.add * exp2f(g2 * (float)(m.rev ? t + 1 : n - 1 - t));
+        for (int g = 0; g < groups; ++g) {
           const bool update = sums || g == groups - 1;
           uint32_t at[3] = {0, 0, 0};
 #pragma unroll
@@ -437,8 +491,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             r.next(C::kSlots);
           }
           const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
+          const uint32_t high = weighted + (updates % C::kBuffers) * C::kWeighted, rest = high + C::kSlot;
           if (update) {
-#pragma unroll 1
+#pragma unroll 2
             for (int x = 0; x < D; x += 8) {
               float v[8], lo[8];
               const uint32_t off = sw128_offset(t, x, kTile);
@@ -452,11 +507,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                   lo[2 * j] = v0 - __uint_as_float(h[j] << 16);
                   lo[2 * j + 1] = v1 - __uint_as_float(h[j] & 0xffff0000u);
                 }
-                st_shared_v4(weighted + off, h[0], h[1], h[2], h[3]);
-                st_bf16x8(weighted + C::kSlot + off, lo);
+                st_shared_v4(high + off, h[0], h[1], h[2], h[3]);
+                st_bf16x8(rest + off, lo);
               } else {
-                st_shared_v4(weighted + off, 0, 0, 0, 0);
-                st_shared_v4(weighted + C::kSlot + off, 0, 0, 0, 0);
+                st_shared_v4(high + off, 0, 0, 0, 0);
+                st_shared_v4(rest + off, 0, 0, 0, 0);
               }
             }
           }
@@ -475,43 +530,25 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
               mbar_arrive(empty + at[o]);
             }
           }
-          if (!update) continue;
-          wait(added, adds & 1);
-          ++adds;
-          if (g < groups - 1) continue;
-          tc_fence_after();
-          const float keep = exp2f(g2 * (float)n);
-          if constexpr (D == 64) {
-            float u[32], v[32];
-            tmem_ld32x2(row_base, row_base + 32, u, v);
-            const bool low = t >= 64;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float *give = low ? u + 4 * i : v + 4 * i;
-              st_shared_v4(exchange + (i * 128 + t) * 16, __float_as_uint(give[0]), __float_as_uint(give[1]),
-                           __float_as_uint(give[2]), __float_as_uint(give[3]));
-            }
-            named_barrier_sync(kBar, 128);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float x[4];
-              ld_shared_v4f(exchange + (i * 128 + (t ^ 64)) * 16, x);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) s[4 * i + j] = fmaf(s[4 * i + j], keep, (low ? v[4 * i + j] : u[4 * i + j]) + x[j]);
+          // With two buffers the rows of the next update are handed out before the last one is waited for.
+          if (update) ++updates;
+          if (C::kBuffers == 1) {
+            if (update) {
+              const bool whole = g == groups - 1;
+              take(whole, keep);
+              if (whole && !total && k < count - 1) publish();
             }
           } else {
-#pragma unroll
-            for (int x = 0; x < D; x += 16) {
-              float u[16];
-              tmem_ld16(row_base + x, u);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) s[x + j] = fmaf(s[x + j], keep, u[j]);
+            if (updates - adds == (update ? 2u : 1u)) {
+              const bool whole = pending_whole;
+              take(whole, pending_keep);
+              if (whole && !total) publish();
             }
+            if (update) pending_whole = g == groups - 1, pending_keep = keep;
           }
-          tc_fence_before();
-          if (!total && k < count - 1) publish();
         }
       }
+      if (C::kBuffers == 2 && updates != adds) take(pending_whole, pending_keep);
       float *end = piece_end(w, m, pc, part);
       if (end && m.transposed) {
 #pragma unroll
