@@ -81,7 +81,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                  exchange = state + C::kBuffers * C::kState;
   uint64_t *bars = reinterpret_cast<uint64_t *>(generic + (exchange - base) + C::kExchange);
   uint64_t *full = bars, *empty = full + C::kSlots, *turned = empty + C::kSlots, *scored = turned + C::kSlots,
-           *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *known = added + 2, *drain = known + 2;
+           *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *whole = added + 2, *known = whole + 2, *drain = known + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -95,13 +95,14 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 2);   // the MMAs, the state's warpgroup
-      mbar_init(turned + i, 1);  // what the MMAs need of the state's warpgroup for these rows
+      mbar_init(empty + i, 2);   // the MMAs, the rows' warpgroup
+      mbar_init(turned + i, 1);  // what the MMAs need of the rows' warpgroup
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(scored + i, 1);
       mbar_init(ready + i, 4);
       mbar_init(added + i, 1);
+      mbar_init(whole + i, 1);
       mbar_init(known + i, 1);
     }
     mbar_init(done, 1);
@@ -197,7 +198,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             const bool last = g == groups - 1, update = sums || last;
             auto read = [&]() {
               if (g == 0) agree(wait(known + tiles % C::kBuffers, (tiles / C::kBuffers) & 1));
-              if (g > 0 && sums) return;
+              if (total || (g > 0 && sums)) return;
               agree(wait(taken, (outs & 1) ^ 1));
               if (alive && elect_lane()) {
                 tc_fence_after();
@@ -241,7 +242,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             }
             // with two buffers the update goes first, ahead of the state that this tile reads; with one it would
             // overwrite what the state's warpgroup has yet to take
-            if (C::kBuffers == 1 && !total) read();
+            if (C::kBuffers == 1) read();
             agree(wait(turned + slot_c, phase_c));
             const uint32_t c = slots + slot_c * C::kSlot;
             if (update) {
@@ -258,6 +259,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                     mma_bf16(d, desc_mnmajor(b + C::kSlot, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update, 1);
                 }
                 mma_commit(added + updates % C::kBuffers);
+                if (last) mma_commit(whole + tiles % C::kBuffers);
                 if (total) {
                   mma_commit(empty + slot_b);
                   mma_commit(empty + slot_c);
@@ -266,7 +268,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
               __syncwarp();
               ++updates;
             }
-            if (C::kBuffers == 2 && !total) read();
+            if (C::kBuffers == 2) read();
             if (!total) {
               const uint32_t sb = unit % C::kBuffers;
               agree(wait(ready + sb, (unit / C::kBuffers) & 1));
@@ -361,47 +363,118 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       }
     }
   } else if (wg == 2) {
-    // ---- results: thread t has row t ---------------------------------------------
+    // ---- rows: thread t has row t, of b to weigh it and of the results to write them ----
     regs_dec<80>();
     const int t = threadIdx.x - 256, q = t >> 5;
     const uint32_t row_base = tmem_addr(tmem, q * 32, 0);
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(m.out);
-    uint32_t outs = 0;
+    Ring r;
+    uint32_t outs = 0, updates = 0;
+    // the result that is to be written next
+    __nv_bfloat16 *dst = nullptr;
+    float read = 0.f;
+    bool due = false, mine = false;
+    auto write = [&]() {
+      if (!due) return;
+      due = false;
+      wait(done, outs & 1);
+      ++outs;
+      tc_fence_after();
+#pragma unroll 1
+      for (int x = 0; x < D; x += 16) {
+        float v[16], u[16];
+        tmem_ld16x2(row_base + C::tRead + x, row_base + C::tWithin + x, v, u);
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          h[j] = pack_bf16(fmaf(v[2 * j], read, m.within * u[2 * j]), fmaf(v[2 * j + 1], read, m.within * u[2 * j + 1]));
+        if (mine) {
+          *reinterpret_cast<uint4 *>(dst + x) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(taken);
+    };
     while (walk.next(w, pc)) {
-      if (total || pc.rows == 0) continue;
+      if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
       const float g2 = log2_decay(p.log_decay, pc.head);
       for (int k = 0; k < pc.t1 - pc.t0; ++k) {
         const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
-        const float read = m.read * exp2f(g2 * (float)(m.rev ? n - 1 - t : t + 1));  // rows past n are not written
-        for (int g = 0; g < (sums ? 1 : groups); ++g, ++outs) {
-          wait(done, outs & 1);
-          tc_fence_after();
-          __nv_bfloat16 *dst = out + ((long long)pc.row0 + tile * kTile + t) * m.out_row + (long long)(pc.head * m.a_heads + g) * D;
-#pragma unroll 1
-          for (int x = 0; x < D; x += 16) {
-            float r[16], v[16];
-            tmem_ld16x2(row_base + C::tRead + x, row_base + C::tWithin + x, r, v);
-            uint32_t u[8];
+        // rows past n are neither weighed nor written
+        const float up = exp2f(g2 * (float)(t + 1)), down = exp2f(g2 * (float)(n - 1 - t)), weight = m.add * (m.rev ? up : down);
+        for (int g = 0; g < groups; ++g) {
+          uint32_t at[3] = {0, 0, 0}, phase[3] = {0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              u[j] = pack_bf16(fmaf(r[2 * j], read, m.within * v[2 * j]), fmaf(r[2 * j + 1], read, m.within * v[2 * j + 1]));
-            if (t < n) {
-              *reinterpret_cast<uint4 *>(dst + x) = make_uint4(u[0], u[1], u[2], u[3]);
-              *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+          for (int o = 0; o < 3; ++o) {
+            if (o == 1 && total) continue;
+            at[o] = r.slot;
+            phase[o] = r.phase;
+            r.next(C::kSlots);
+          }
+          const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
+          wait(full + at[0], phase[0]);
+          if (sums || g == groups - 1) {
+            const uint32_t high = weighted + (updates % C::kBuffers) * C::kWeighted, rest = high + C::kSlot;
+            if (updates >= C::kBuffers) wait(added + updates % C::kBuffers, (updates / C::kBuffers + 1) & 1);
+            ++updates;
+#pragma unroll 2
+            for (int x = 0; x < D; x += 8) {
+              float v[8], lo[8];
+              const uint32_t off = sw128_offset(t, x, kTile);
+              if (t < n) {
+                ld_bf16x8(b + off, v);
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float v0 = v[2 * j] * weight, v1 = v[2 * j + 1] * weight;
+                  h[j] = pack_bf16(v0, v1);
+                  lo[2 * j] = v0 - __uint_as_float(h[j] << 16);
+                  lo[2 * j + 1] = v1 - __uint_as_float(h[j] & 0xffff0000u);
+                }
+                st_shared_v4(high + off, h[0], h[1], h[2], h[3]);
+                st_bf16x8(rest + off, lo);
+              } else {
+                st_shared_v4(high + off, 0, 0, 0, 0);
+                st_shared_v4(rest + off, 0, 0, 0, 0);
+              }
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(taken);
+          if (!total) wait(full + at[1], phase[1]);
+          wait(full + at[2], phase[2]);
+          if (t >= n) {
+            // rows behind the sequence: 0 times whatever they hold has to be 0
+#pragma unroll 1
+            for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+          }
+          fence_async_smem();
+          named_barrier_sync(2, 128);
+          if (t == 0) {
+#pragma unroll
+            for (int o = 0; o < 3; ++o) {
+              if (o == 1 && total) continue;
+              mbar_arrive(turned + at[o]);  // every slot's, so that its phases go with the loads'
+              mbar_arrive(empty + at[o]);
+            }
+          }
+          // the last unit's result, while the MMAs take what was handed out
+          write();
+          due = !total && (!sums || g == groups - 1);
+          if (due) {
+            dst = static_cast<__nv_bfloat16 *>(m.out) + ((long long)pc.row0 + tile * kTile + t) * m.out_row +
+                  (long long)(pc.head * m.a_heads + (sums ? 0 : g)) * D;
+            read = m.read * (m.rev ? down : up);
+            mine = t < n;
+          }
         }
       }
     }
+    write();
   } else {
     // ---- the state -----------------------------------------------------------------
-    // Thread t weighs row t of b.  Of the state it has row t (D = 128), or
-    // half of row t % 64: with D = 64 the update's rows 0-63 are those of the
-    // high parts and 64-127 those of the remainders, so two threads exchange
-    // halves and add.
+    // Thread t has row t of it (D = 128), or half of row t % 64: with D = 64
+    // the update's rows 0-63 are those of the high parts and 64-127 those of
+    // the remainders, so two threads exchange halves and add.
     regs_inc<208>();
     constexpr int kOwn = D == 64 ? 32 : 128;
     const int t = threadIdx.x - 384, q = t >> 5;
@@ -409,22 +482,20 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     const uint32_t row_base = tmem_addr(tmem, q * 32, C::tUpdate);
     constexpr int kBar = 1;
     float s[kOwn];
-    Ring r;
-    uint32_t adds = 0, updates = 0, tiles = 0;  // updates waited for, handed out; tiles whose state is published
+    uint32_t tiles = 0, summed = 0;  // tiles whose state is published, whose update is in the state
     auto publish = [&]() {  // the state as the operand [x][y]
       const uint32_t buffer = tiles++ % C::kBuffers, x = state + buffer * C::kState;
+      if (!total) {
 #pragma unroll
-      for (int i = 0; i < kOwn; i += 8) st_bf16x8(x + sw128_offset(srow, scol + i, D), s + i);
-      fence_async_smem();
+        for (int i = 0; i < kOwn; i += 8) st_bf16x8(x + sw128_offset(srow, scol + i, D), s + i);
+        fence_async_smem();
+      }
       named_barrier_sync(kBar, 128);
       if (t == 0) mbar_arrive(known + buffer);
     };
-    uint32_t summed = 0;  // tiles whose update is in the state
-    // Waits for the oldest update handed out; where it is its tile's last, the state takes the tile's sum.
-    auto take = [&](bool whole, float keep) {
-      wait(added + adds % C::kBuffers, (adds / C::kBuffers) & 1);
-      ++adds;
-      if (!whole) return;
+    // The state takes a tile's update.
+    auto take = [&](float keep) {
+      wait(whole + summed % C::kBuffers, (summed / C::kBuffers) & 1);
       tc_fence_after();
       const uint32_t from = row_base + (summed % C::kBuffers) * D;
       ++summed;
@@ -474,81 +545,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         for (int i = 0; i < kOwn; ++i) s[i] = start[first + i];
       }
       const int count = pc.rows == 0 ? 0 : pc.t1 - pc.t0;
-      bool pending_whole = false;
-      float pending_keep = 0.f;
-      if (!total && count) publish();
       for (int k = 0; k < count; ++k) {
         const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
-        const float keep = exp2f(g2 * (float)n), weight = m.add * exp2f(g2 * (float)(m.rev ? t + 1 : n - 1 - t));
-        for (int g = 0; g < groups; ++g) {
-          const bool update = sums || g == groups - 1;
-          uint32_t at[3] = {0, 0, 0};
-#pragma unroll
-          for (int o = 0; o < 3; ++o) {
-            if (o == 1 && total) continue;
-            wait(full + r.slot, r.phase);
-            at[o] = r.slot;
-            r.next(C::kSlots);
-          }
-          const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
-          const uint32_t high = weighted + (updates % C::kBuffers) * C::kWeighted, rest = high + C::kSlot;
-          if (update) {
-#pragma unroll 2
-            for (int x = 0; x < D; x += 8) {
-              float v[8], lo[8];
-              const uint32_t off = sw128_offset(t, x, kTile);
-              if (t < n) {
-                ld_bf16x8(b + off, v);
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float v0 = v[2 * j] * weight, v1 = v[2 * j + 1] * weight;
-                  h[j] = pack_bf16(v0, v1);
-                  lo[2 * j] = v0 - __uint_as_float(h[j] << 16);
-                  lo[2 * j + 1] = v1 - __uint_as_float(h[j] & 0xffff0000u);
-                }
-                st_shared_v4(high + off, h[0], h[1], h[2], h[3]);
-                st_bf16x8(rest + off, lo);
-              } else {
-                st_shared_v4(high + off, 0, 0, 0, 0);
-                st_shared_v4(rest + off, 0, 0, 0, 0);
-              }
-            }
-          }
-          if (t >= n) {
-            // rows behind the sequence: 0 times whatever they hold has to be 0
-#pragma unroll 1
-            for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
-          }
-          fence_async_smem();
-          named_barrier_sync(kBar, 128);
-          if (t == 0) {
-#pragma unroll
-            for (int o = 0; o < 3; ++o) {
-              if (o == 1 && total) continue;
-              mbar_arrive(turned + at[o]);  // every slot's, so that its phases go with the loads'
-              mbar_arrive(empty + at[o]);
-            }
-          }
-          // With two buffers the rows of the next update are handed out before the last one is waited for.
-          if (update) ++updates;
-          if (C::kBuffers == 1) {
-            if (update) {
-              const bool whole = g == groups - 1;
-              take(whole, keep);
-              if (whole && !total && k < count - 1) publish();
-            }
-          } else {
-            if (updates - adds == (update ? 2u : 1u)) {
-              const bool whole = pending_whole;
-              take(whole, pending_keep);
-              if (whole && !total) publish();
-            }
-            if (update) pending_whole = g == groups - 1, pending_keep = keep;
-          }
-        }
+        publish();
+        take(exp2f(g2 * (float)n));
       }
-      if (C::kBuffers == 2 && updates != adds) take(pending_whole, pending_keep);
       float *end = piece_end(w, m, pc, part);
       if (end && m.transposed) {
 #pragma unroll
