@@ -159,38 +159,49 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       // ---- MMAs ------------------------------------------------------------------
       const uint32_t id_scores = make_idesc(128, 128, false, false), id_state = make_idesc(128, D, false, true),
                      id_update = make_idesc(128, D, true, true);
-      Ring r;                    // the next unit whose scores are to be issued
-      uint32_t slot_a = 0, slot_b = 0, slot_c = 0, phase_c = 0;
-      uint32_t ahead[3] = {0, 0, 0}, ahead_phase[3] = {0, 0, 0};
+      // The warp runs converged and one lane issues: descriptors are a constant and a slot's offset, in uniform
+      // registers.  Formed by the issuing lane alone they took three times as long as the MMAs.
+      const bool issues = elect_lane();
+      const uint64_t rows_k = desc_kmajor(slots, kTile, 0, 0), rows_mn = desc_mnmajor(slots, kTile, 0, 0),
+                     weighted_mn = desc_mnmajor(weighted, kTile, 0, 0), state_mn = desc_mnmajor(state, D, 0, 0);
+      constexpr uint32_t kSlotStep = C::kSlot >> 4;
       bool alive = true;
-      uint32_t units_scored = 0, unit = 0, outs = 0, tiles = 0, updates = 0;
-      auto agree = [&](bool ok) { alive = alive && __all_sync(0xffffffffu, ok); return alive; };
-      // the slots of the unit at the ring's place
-      auto place = [&]() {
-        Ring t = r;
-        const int n = total ? 2 : 3;
-        for (int o = 0; o < n; ++o) {
-          const int at = total && o == 1 ? 2 : o;
-          ahead[at] = t.slot;
-          ahead_phase[at] = t.phase;
+      auto agree = [&](bool ok) { alive = alive && __all_sync(0xffffffffu, ok); };
+      // A unit's slots, as the ring gives them: b, a, c (b, c).
+      struct Unit {
+        uint32_t b, pb, a, pa, c, pc;
+      };
+      auto unit_at = [&](Ring &t) {
+        Unit u{};
+        u.b = t.slot, u.pb = t.phase;
+        t.next(C::kSlots);
+        if (!total) {
+          u.a = t.slot, u.pa = t.phase;
           t.next(C::kSlots);
         }
-        return t;
+        u.c = t.slot, u.pc = t.phase;
+        t.next(C::kSlots);
+        return u;
       };
-      auto scores = [&]() {  // of unit `units_scored`, at `ahead`
-        if (alive && elect_lane()) {
-          const uint32_t a = slots + ahead[1] * C::kSlot, b = slots + ahead[0] * C::kSlot;
-          const uint32_t d = tmem + C::tScores + (units_scored % C::kBuffers) * 128;
-          tc_fence_after();
+      uint32_t scored_units = 0;
+      auto scores = [&](const Unit &u) {
+        const uint32_t buffer = scored_units++ % C::kBuffers, d = tmem + C::tScores + buffer * 128;
+        if (!alive) return;
+        tc_fence_after();
+        const uint64_t a = rows_k + u.a * kSlotStep, b = rows_k + u.b * kSlotStep;
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) mma_bf16(d, desc_kmajor(a, kTile, 0, s), desc_kmajor(b, kTile, 0, s), id_scores, s > 0);
-          mma_commit(scored + units_scored % C::kBuffers);
-          mma_commit(empty + ahead[0]);
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t at = (s >> 2) * kTile * 8u + (s & 3) * 2u;
+          if (issues) mma_bf16(d, a + at, b + at, id_scores, s > 0);
         }
+        if (issues) mma_commit(scored + buffer);
+        if (issues) mma_commit(empty + u.b);
         __syncwarp();
-        ++units_scored;
       };
-      uint32_t held_a[2] = {0, 0}, held_c[2] = {0, 0}, held_cp[2] = {0, 0};  // slots of units whose scores are issued
+      Ring r;  // the first load of the unit behind those whose scores are issued
+      Unit now{}, then{};
+      bool ahead = false;  // the scores of `then` are issued
+      uint32_t unit = 0, outs = 0, tiles = 0, updates = 0;
       while (walk.next(w, pc)) {
         if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
         for (int k = 0; k < pc.t1 - pc.t0; ++k, ++tiles) {
@@ -200,97 +211,91 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
               if (g == 0) agree(wait(known + tiles % C::kBuffers, (tiles / C::kBuffers) & 1));
               if (total || (g > 0 && sums)) return;
               agree(wait(taken, (outs & 1) ^ 1));
-              if (alive && elect_lane()) {
-                tc_fence_after();
-                const uint32_t a = slots + slot_a * C::kSlot, x = state + (tiles % C::kBuffers) * C::kState;
+              if (!alive) return;
+              tc_fence_after();
+              const uint64_t a = rows_k + now.a * kSlotStep, x = state_mn + (tiles % C::kBuffers) * (C::kState >> 4);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                  mma_bf16(tmem + C::tRead, desc_kmajor(a, kTile, 0, s), desc_mnmajor(x, D, 0, s), id_state, s > 0);
+              for (int s = 0; s < D / 16; ++s) {
+                const uint32_t at = (s >> 2) * kTile * 8u + (s & 3) * 2u;
+                if (issues) mma_bf16(tmem + C::tRead, a + at, x + s * 128u, id_state, s > 0);
               }
               __syncwarp();
             };
-            if (total) {
-              const Ring after = place();
-              slot_b = ahead[0], slot_c = ahead[2], phase_c = ahead_phase[2];
-              r = after;
-              agree(wait(full + slot_b, ahead_phase[0]));
-              agree(wait(full + slot_c, phase_c));
+            if (ahead) {
+              now = then;
+              ahead = false;
             } else {
-              // scores of this unit, if they are not under way
-              if (units_scored == unit) {
-                const Ring after = place();
-                agree(wait(full + ahead[0], ahead_phase[0]));
-                agree(wait(full + ahead[1], ahead_phase[1]));
-                held_a[unit & 1] = ahead[1], held_c[unit & 1] = ahead[2], held_cp[unit & 1] = ahead_phase[2];
-                scores();
-                r = after;
+              now = unit_at(r);
+              agree(wait(full + now.b, now.pb));
+              if (!total) {
+                agree(wait(full + now.a, now.pa));
+                scores(now);
               }
-              slot_a = held_a[unit & 1], slot_c = held_c[unit & 1], phase_c = held_cp[unit & 1];
-              agree(wait(full + slot_c, phase_c));
-              // and those of the next one, if its rows are here: whether there is a next one shows in the
-              // barrier alone, which completes no phase without a load
-              if (C::kBuffers == 2 && units_scored == unit + 1) {
-                const Ring after = place();
-                const bool here = __shfl_sync(0xffffffffu, (int)(mbar_test(full + ahead[0], ahead_phase[0]) &&
-                                                                 mbar_test(full + ahead[1], ahead_phase[1])), 0);
-                if (here && alive) {
-                  held_a[(unit + 1) & 1] = ahead[1], held_c[(unit + 1) & 1] = ahead[2], held_cp[(unit + 1) & 1] = ahead_phase[2];
-                  scores();
-                  r = after;
-                }
+            }
+            agree(wait(full + now.c, now.pc));
+            // the scores of the next unit, if its rows are here: whether there is a next one shows in the barrier
+            // alone, which completes no phase without a load
+            if (C::kBuffers == 2 && !total) {
+              Ring t = r;
+              const Unit u = unit_at(t);
+              const bool here = mbar_test(full + u.b, u.pb) && mbar_test(full + u.a, u.pa);
+              if (__all_sync(0xffffffffu, here) && alive) {
+                then = u;
+                r = t;
+                ahead = true;
+                scores(u);
               }
             }
             // with two buffers the update goes first, ahead of the state that this tile reads; with one it would
             // overwrite what the state's warpgroup has yet to take
             if (C::kBuffers == 1) read();
-            agree(wait(turned + slot_c, phase_c));
-            const uint32_t c = slots + slot_c * C::kSlot;
+            agree(wait(turned + now.c, now.pc));
+            const uint64_t c = rows_mn + now.c * kSlotStep;
             if (update) {
-              if (alive && elect_lane()) {
+              if (alive) {
                 tc_fence_after();
                 const bool first = !sums || g == 0;
-                const uint32_t d = tmem + C::tUpdate + (tiles % C::kBuffers) * D, b = weighted + (updates % C::kBuffers) * C::kWeighted;
+                const uint32_t d = tmem + C::tUpdate + (tiles % C::kBuffers) * D;
+                const uint64_t b = weighted_mn + (updates % C::kBuffers) * (C::kWeighted >> 4);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  mma_bf16(d, desc_mnmajor(b, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update, s > 0 || !first);
+                  if (issues) mma_bf16(d, b + s * 128u, c + s * 128u, id_update, s > 0 || !first);
                 if constexpr (D == 128) {
 #pragma unroll
                   for (int s = 0; s < 8; ++s)
-                    mma_bf16(d, desc_mnmajor(b + C::kSlot, kTile, 0, s), desc_mnmajor(c, kTile, 0, s), id_update, 1);
+                    if (issues) mma_bf16(d, b + kSlotStep + s * 128u, c + s * 128u, id_update, 1);
                 }
-                mma_commit(added + updates % C::kBuffers);
-                if (last) mma_commit(whole + tiles % C::kBuffers);
-                if (total) {
-                  mma_commit(empty + slot_b);
-                  mma_commit(empty + slot_c);
-                }
+                if (issues) mma_commit(added + updates % C::kBuffers);
+                if (last && issues) mma_commit(whole + tiles % C::kBuffers);
+                if (total && issues) mma_commit(empty + now.b);
+                if (total && issues) mma_commit(empty + now.c);
+                __syncwarp();
               }
-              __syncwarp();
               ++updates;
             }
             if (C::kBuffers == 2) read();
             if (!total) {
-              const uint32_t sb = unit % C::kBuffers;
-              agree(wait(ready + sb, (unit / C::kBuffers) & 1));
-              if (alive && elect_lane()) {
+              const uint32_t buffer = unit % C::kBuffers;
+              agree(wait(ready + buffer, (unit / C::kBuffers) & 1));
+              if (alive) {
                 tc_fence_after();
                 const bool first = !sums || g == 0;
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  mma_bf16_ta(tmem + C::tWithin, tmem + C::tScores + sb * 128 + s * 8, desc_mnmajor(c, kTile, 0, s), id_state,
-                              s > 0 || !first);
-                mma_commit(empty + slot_a);
-                mma_commit(empty + slot_c);
-                if (last || !sums) mma_commit(done);
+                  if (issues)
+                    mma_bf16_ta(tmem + C::tWithin, tmem + C::tScores + buffer * 128 + s * 8, c + s * 128u, id_state, s > 0 || !first);
+                if (issues) mma_commit(empty + now.a);
+                if (issues) mma_commit(empty + now.c);
+                if ((last || !sums) && issues) mma_commit(done);
+                __syncwarp();
               }
-              __syncwarp();
               if (last || !sums) ++outs;
             }
           }
         }
       }
       // what was issued has to end before its tensor memory goes
-      if (elect_lane()) {
+      if (issues) {
         mma_commit(drain);
         mbar_drain(drain, 0);
       }
