@@ -18,9 +18,9 @@
 // state stays in fp32 registers, and b~ enters as two bf16 numbers (high part
 // and remainder, 2^-17), because states are results in fp32 too.
 //
-// Four roles: one warp loads tiles by TMA into a ring, one issues the MMAs,
-// and three warpgroups form the weighted scores, write the results, and keep
-// the state.  The bound is memory: 128 rows of four arrays take 2900 cycles of
+// Roles: one warp loads tiles by TMA into a ring, two issue the MMAs, and
+// three warpgroups form the weighted scores; weigh b's rows and write the
+// results; and keep the state.  The bound is memory: 128 rows of four arrays take 2900 cycles of
 // this SM's share of HBM at D = 64 (5800 at 128), the products of a unit 1400
 // (2700).
 #include <cuda.h>
@@ -40,22 +40,25 @@ using q8::regs_dec;
 using q8::regs_inc;
 
 constexpr int kTile = 128, kThreads = 512;
+constexpr uint32_t kGiveUp = 1u << 21;  // tries of a wait, each of which may sleep for a while: a second or more
+constexpr int kUnits = 4;  // barriers of units in a row: more than the ring holds
 
 template <int D> struct Cfg {
   static constexpr uint32_t kSlot = kTile * D * 2;     // a tile of one operand
-  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kSlots = D == 64 ? 8 : 5;
   static constexpr int kBuffers = D == 64 ? 2 : 1;     // of scores, b~, X and updates
-  static constexpr uint32_t kWeighted = 2 * kSlot;     // b~: high parts and remainders
+  static constexpr bool kInPlace = D == 128;           // high parts of b~ take b's place, when the scores are done
+  static constexpr uint32_t kWeighted = kInPlace ? kSlot : 2 * kSlot;  // b~: (high parts and) remainders
   static constexpr uint32_t kState = D * D * 2;
   static constexpr uint32_t kExchange = D == 64 ? 16384 : 0;
-  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kBuffers * (kWeighted + kState) + kExchange + 512;
+  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kBuffers * (kWeighted + kState) + kExchange + 1024;
   // tensor memory columns
   static constexpr uint32_t tScores = 0, tRead = 128 * kBuffers, tWithin = tRead + D, tUpdate = tWithin + D;
   static_assert(tUpdate + kBuffers * D <= 512, "tensor memory");
 };
 
 struct Args {
-  CUtensorMap maps[4];
+  CUtensorMap maps[4], outs[3];
   Work work;
   const float *log_decay;
   int *status;
@@ -80,10 +83,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
   const uint32_t slots = base, weighted = slots + C::kSlots * C::kSlot, state = weighted + C::kBuffers * C::kWeighted,
                  exchange = state + C::kBuffers * C::kState;
   uint64_t *bars = reinterpret_cast<uint64_t *>(generic + (exchange - base) + C::kExchange);
-  uint64_t *full = bars, *empty = full + C::kSlots, *turned = empty + C::kSlots, *scored = turned + C::kSlots,
+  uint64_t *full = bars, *turned = full + kUnits, *empty = turned + kUnits, *scored = empty + C::kSlots,
            *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *whole = added + 2, *known = whole + 2, *drain = known + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  float *powers = reinterpret_cast<float *>(generic + (exchange - base) + C::kExchange + 512);  // lambda^0 .. lambda^127
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
   const int part = blockIdx.x / p.mixes, which = blockIdx.x - part * p.mixes;
@@ -94,9 +98,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 2);   // the MMAs, the rows' warpgroup
-      mbar_init(turned + i, 1);  // what the MMAs need of the rows' warpgroup
+      mbar_init(empty + i, total ? 5 : 6);  // each issuing warp, each warp of the rows' warpgroup
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(full + i, total ? 2 : 3);  // the unit's operands
+      mbar_init(turned + i, 1);            // what the MMAs need of the rows' warpgroup
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(scored + i, 1);
@@ -105,9 +111,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       mbar_init(whole + i, 1);
       mbar_init(known + i, 1);
     }
-    mbar_init(done, 1);
+    mbar_init(done, 2);
     mbar_init(taken, 4);
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     *abort = 0;
     fence_barrier_init();
   }
@@ -122,7 +129,15 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
   // MMAs, so that none is missed at a barrier of its warpgroup.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
-    return !*abort && mbar_wait(bar, parity, p.status, abort);
+    if (*abort) return false;
+    // Short, because there are many, and the caches have to hold the instructions of all the roles at once.
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+      if (i & 255u) continue;
+      if (i >= kGiveUp) atomicCAS(p.status, 0, 5), *abort = 1;
+      if (*abort) return false;
+    }
+    return true;
   };
 
   Walk walk(w, part, m.rev);
@@ -134,20 +149,22 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       const CUtensorMap *maps[3] = {p.maps + p.b[which], p.maps + (total ? 0 : p.a[which]), p.maps + p.c[which]};
       const int b_heads = m.b_heads, a_heads = m.a_heads;
       Ring r;
+      uint32_t unit = 0;
       while (walk.next(w, pc)) {
         if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
         for (int k = 0; k < pc.t1 - pc.t0; ++k) {
           const int row = pc.row0 + (m.rev ? pc.t1 - 1 - k : pc.t0 + k) * kTile;
-          for (int g = 0; g < groups; ++g) {
+          for (int g = 0; g < groups; ++g, ++unit) {
+            uint64_t *bar = full + unit % kUnits;
             const int hb = pc.head * b_heads + (b_heads > 1 ? g : 0), ha = pc.head * a_heads + (a_heads > 1 ? g : 0);
 #pragma unroll
             for (int o = 0; o < 3; ++o) {
               if (o == 1 && total) continue;
               const bool ok = __all_sync(0xffffffffu, wait(empty + r.slot, r.phase ^ 1));
               if (ok && elect_lane()) {
-                mbar_arrive_expect_tx(full + r.slot, C::kSlot);
+                mbar_arrive_expect_tx(bar, C::kSlot);
                 for (int x = 0; x < D / 64; ++x)
-                  tma_load_3d(generic + r.slot * C::kSlot + x * 16384, maps[o], full + r.slot, x * 64, o == 1 ? ha : hb, row);
+                  tma_load_3d(generic + r.slot * C::kSlot + x * 16384, maps[o], bar, x * 64, o == 1 ? ha : hb, row);
               }
               __syncwarp();
               r.next(C::kSlots);
@@ -155,130 +172,89 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           }
         }
       }
-    } else if (warp == 1) {
-      // ---- MMAs ------------------------------------------------------------------
-      const uint32_t id_scores = make_idesc(128, 128, false, false), id_state = make_idesc(128, D, false, true),
-                     id_update = make_idesc(128, D, true, true);
-      // The warp runs converged and one lane issues: descriptors are a constant and a slot's offset, in uniform
+    } else if (warp < 3) {
+      // ---- MMAs: warp 1 issues scores and products of weighted scores, warp 2 updates and reads ----
+      // Two warps, because an MMA holds up its issuing thread while it runs, and each of the waits between
+      // them costs some fifty cycles more (one warp for all: 4400 cycles a unit at D = 64, 3000 of them busy).
+      // A warp runs converged and one lane issues: descriptors are a constant and a slot's offset, in uniform
       // registers.  Formed by the issuing lane alone they took three times as long as the MMAs.
       const bool issues = elect_lane();
       const uint64_t rows_k = desc_kmajor(slots, kTile, 0, 0), rows_mn = desc_mnmajor(slots, kTile, 0, 0),
                      weighted_mn = desc_mnmajor(weighted, kTile, 0, 0), state_mn = desc_mnmajor(state, D, 0, 0);
       constexpr uint32_t kSlotStep = C::kSlot >> 4;
+      const uint32_t id_scores = make_idesc(128, 128, false, false), id_state = make_idesc(128, D, false, true),
+                     id_update = make_idesc(128, D, true, true);
       bool alive = true;
       auto agree = [&](bool ok) { alive = alive && __all_sync(0xffffffffu, ok); };
       // A unit's slots, as the ring gives them: b, a, c (b, c).
       struct Unit {
-        uint32_t b, pb, a, pa, c, pc;
+        uint32_t b, a, c;
       };
       auto unit_at = [&](Ring &t) {
         Unit u{};
-        u.b = t.slot, u.pb = t.phase;
+        u.b = t.slot;
         t.next(C::kSlots);
         if (!total) {
-          u.a = t.slot, u.pa = t.phase;
+          u.a = t.slot;
           t.next(C::kSlots);
         }
-        u.c = t.slot, u.pc = t.phase;
+        u.c = t.slot;
         t.next(C::kSlots);
         return u;
       };
-      uint32_t scored_units = 0;
-      auto scores = [&](const Unit &u) {
-        const uint32_t buffer = scored_units++ % C::kBuffers, d = tmem + C::tScores + buffer * 128;
-        if (!alive) return;
-        tc_fence_after();
-        const uint64_t a = rows_k + u.a * kSlotStep, b = rows_k + u.b * kSlotStep;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t at = (s >> 2) * kTile * 8u + (s & 3) * 2u;
-          if (issues) mma_bf16(d, a + at, b + at, id_scores, s > 0);
-        }
-        if (issues) mma_commit(scored + buffer);
-        if (issues) mma_commit(empty + u.b);
-        __syncwarp();
-      };
-      Ring r;  // the first load of the unit behind those whose scores are issued
-      Unit now{}, then{};
-      bool ahead = false;  // the scores of `then` are issued
+      Ring r;
       uint32_t unit = 0, outs = 0, tiles = 0, updates = 0;
-      while (walk.next(w, pc)) {
-        if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
-        for (int k = 0; k < pc.t1 - pc.t0; ++k, ++tiles) {
-          for (int g = 0; g < groups; ++g, ++unit) {
-            const bool last = g == groups - 1, update = sums || last;
-            auto read = [&]() {
-              if (g == 0) agree(wait(known + tiles % C::kBuffers, (tiles / C::kBuffers) & 1));
-              if (total || (g > 0 && sums)) return;
-              agree(wait(taken, (outs & 1) ^ 1));
-              if (!alive) return;
-              tc_fence_after();
-              const uint64_t a = rows_k + now.a * kSlotStep, x = state_mn + (tiles % C::kBuffers) * (C::kState >> 4);
+      if (warp == 1 && !total) {
+        uint32_t scored_units = 0;
+        auto scores = [&](const Unit &u) {
+          const uint32_t buffer = scored_units++ % C::kBuffers, d = tmem + C::tScores + buffer * 128;
+          if (!alive) return;
+          tc_fence_after();
+          const uint64_t a = rows_k + u.a * kSlotStep, b = rows_k + u.b * kSlotStep;
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s) {
-                const uint32_t at = (s >> 2) * kTile * 8u + (s & 3) * 2u;
-                if (issues) mma_bf16(tmem + C::tRead, a + at, x + s * 128u, id_state, s > 0);
-              }
-              __syncwarp();
-            };
-            if (ahead) {
-              now = then;
-              ahead = false;
-            } else {
-              now = unit_at(r);
-              agree(wait(full + now.b, now.pb));
-              if (!total) {
-                agree(wait(full + now.a, now.pa));
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t at = (s >> 2) * kTile * 8u + (s & 3) * 2u;
+            if (issues) mma_bf16(d, a + at, b + at, id_scores, s > 0);
+          }
+          if (issues) mma_commit(scored + buffer);
+          if (issues) mma_commit(empty + u.b);
+          __syncwarp();
+        };
+        Unit now{}, then{};
+        bool ahead = false;  // the scores of `then` are issued; r is behind it
+        while (walk.next(w, pc)) {
+          if (pc.rows == 0) continue;
+          for (int k = 0; k < pc.t1 - pc.t0; ++k) {
+            for (int g = 0; g < groups; ++g, ++unit) {
+              const bool last = g == groups - 1;
+              if (ahead) {
+                now = then;
+                ahead = false;
+              } else {
+                now = unit_at(r);
+                agree(wait(full + unit % kUnits, (unit / kUnits) & 1));
                 scores(now);
               }
-            }
-            agree(wait(full + now.c, now.pc));
-            // the scores of the next unit, if its rows are here: whether there is a next one shows in the barrier
-            // alone, which completes no phase without a load
-            if (C::kBuffers == 2 && !total) {
-              Ring t = r;
-              const Unit u = unit_at(t);
-              const bool here = mbar_test(full + u.b, u.pb) && mbar_test(full + u.a, u.pa);
-              if (__all_sync(0xffffffffu, here) && alive) {
-                then = u;
-                r = t;
-                ahead = true;
-                scores(u);
-              }
-            }
-            // with two buffers the update goes first, ahead of the state that this tile reads; with one it would
-            // overwrite what the state's warpgroup has yet to take
-            if (C::kBuffers == 1) read();
-            agree(wait(turned + now.c, now.pc));
-            const uint64_t c = rows_mn + now.c * kSlotStep;
-            if (update) {
-              if (alive) {
-                tc_fence_after();
-                const bool first = !sums || g == 0;
-                const uint32_t d = tmem + C::tUpdate + (tiles % C::kBuffers) * D;
-                const uint64_t b = weighted_mn + (updates % C::kBuffers) * (C::kWeighted >> 4);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                  if (issues) mma_bf16(d, b + s * 128u, c + s * 128u, id_update, s > 0 || !first);
-                if constexpr (D == 128) {
-#pragma unroll
-                  for (int s = 0; s < 8; ++s)
-                    if (issues) mma_bf16(d, b + kSlotStep + s * 128u, c + s * 128u, id_update, 1);
+              // the scores of the next unit, if its rows are here: whether there is a next one shows in the barrier
+              // alone, which completes no phase without loads
+              if (C::kBuffers == 2) {
+                Ring t = r;
+                const Unit u = unit_at(t);
+                const bool here = mbar_test(full + (unit + 1) % kUnits, ((unit + 1) / kUnits) & 1);
+                if (__all_sync(0xffffffffu, here) && alive) {
+                  then = u;
+                  r = t;
+                  ahead = true;
+                  scores(u);
                 }
-                if (issues) mma_commit(added + updates % C::kBuffers);
-                if (last && issues) mma_commit(whole + tiles % C::kBuffers);
-                if (total && issues) mma_commit(empty + now.b);
-                if (total && issues) mma_commit(empty + now.c);
-                __syncwarp();
               }
-              ++updates;
-            }
-            if (C::kBuffers == 2) read();
-            if (!total) {
               const uint32_t buffer = unit % C::kBuffers;
+              agree(wait(turned + unit % kUnits, (unit / kUnits) & 1));
               agree(wait(ready + buffer, (unit / C::kBuffers) & 1));
+              if (g == 0 || !sums) agree(wait(taken, (outs & 1) ^ 1));
               if (alive) {
                 tc_fence_after();
+                const uint64_t c = rows_mn + now.c * kSlotStep;
                 const bool first = !sums || g == 0;
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
@@ -293,11 +269,73 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             }
           }
         }
+      } else if (warp == 2) {
+        while (walk.next(w, pc)) {
+          if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
+          for (int k = 0; k < pc.t1 - pc.t0; ++k, ++tiles) {
+            for (int g = 0; g < groups; ++g, ++unit) {
+              const bool last = g == groups - 1, update = sums || last;
+              const Unit now = unit_at(r);
+              uint64_t *bar = full + unit % kUnits;
+              const uint32_t phase = (unit / kUnits) & 1;
+              auto read = [&]() {
+                if (g == 0) agree(wait(known + tiles % C::kBuffers, (tiles / C::kBuffers) & 1));
+                if (total) return;
+                if (g == 0 || !sums) {
+                  agree(wait(bar, phase));
+                  agree(wait(taken, (outs & 1) ^ 1));
+                  ++outs;
+                  if (alive) {
+                    tc_fence_after();
+                    const uint64_t a = rows_k + now.a * kSlotStep, x = state_mn + (tiles % C::kBuffers) * (C::kState >> 4);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                      const uint32_t at = (s >> 2) * kTile * 8u + (s & 3) * 2u;
+                      if (issues) mma_bf16(tmem + C::tRead, a + at, x + s * 128u, id_state, s > 0);
+                    }
+                    if (issues) mma_commit(done);
+                  }
+                }
+                if (alive && issues) mma_commit(empty + now.a);
+                __syncwarp();
+              };
+              // with two buffers the update goes first, ahead of the state that this tile reads; with one it would
+              // overwrite what the state's warpgroup has yet to take
+              if (C::kBuffers == 1) read();
+              agree(wait(bar, phase));
+              agree(wait(turned + unit % kUnits, phase));
+              if (alive) {
+                tc_fence_after();
+                if (update) {
+                  const bool first = !sums || g == 0;
+                  const uint32_t d = tmem + C::tUpdate + (tiles % C::kBuffers) * D;
+                  const uint64_t c = rows_mn + now.c * kSlotStep, rest = weighted_mn + (updates % C::kBuffers) * (C::kWeighted >> 4),
+                                 high = C::kInPlace ? rows_mn + now.b * kSlotStep : rest;
+#pragma unroll
+                  for (int s = 0; s < 8; ++s)
+                    if (issues) mma_bf16(d, high + s * 128u, c + s * 128u, id_update, s > 0 || !first);
+                  if constexpr (D == 128) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                      if (issues) mma_bf16(d, rest + s * 128u, c + s * 128u, id_update, 1);
+                  }
+                  if (issues) mma_commit(added + updates % C::kBuffers);
+                  if (last && issues) mma_commit(whole + tiles % C::kBuffers);
+                }
+                if (issues) mma_commit(empty + now.b);
+                if (issues) mma_commit(empty + now.c);
+                __syncwarp();
+              }
+              if (update) ++updates;
+              if (C::kBuffers == 2) read();
+            }
+          }
+        }
       }
       // what was issued has to end before its tensor memory goes
       if (issues) {
-        mma_commit(drain);
-        mbar_drain(drain, 0);
+        mma_commit(drain + warp - 1);
+        mbar_drain(drain + warp - 1, 0);
       }
       __syncwarp();
     }
@@ -309,56 +347,39 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     while (walk.next(w, pc)) {
       if (total || pc.rows == 0) continue;
       const float g2 = log2_decay(p.log_decay, pc.head);
-      // Powers of lambda: from a column to the block's end that is nearer the rows, and on the diagonal block.
-      float2 col[16], diag[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int j0 = 2 * j, j1 = 2 * j + 1;
-        col[j] = make_float2(exp2f(g2 * (float)(m.rev ? j0 : 31 - j0)), exp2f(g2 * (float)(m.rev ? j1 : 31 - j1)));
-        diag[j] = make_float2(exp2f(g2 * fmaxf(0.f, (float)(m.rev ? j0 - lane : lane - j0))),
-                              exp2f(g2 * fmaxf(0.f, (float)(m.rev ? j1 - lane : lane - j1))));
-      }
+      named_barrier_sync(3, 128);
+      powers[t] = exp2f(g2 * (float)t);
+      named_barrier_sync(3, 128);
       for (int k = 0; k < pc.t1 - pc.t0; ++k) {
         const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
         for (int g = 0; g < groups; ++g, ++unit) {
           const uint32_t sb = unit % C::kBuffers, at = row_base + sb * 128;
           wait(scored + sb, (unit / C::kBuffers) & 1);
           tc_fence_after();
+          // Sixteen columns at a time: a warp's rows have consecutive powers in a column.  Rolled: unrolled, and with
+          // powers in registers, the block's code was past the instruction caches, and everything in it three times
+          // as slow.
 #pragma unroll 1
-          for (int jb = 0; jb < 4; ++jb) {
-            float v[32];
-            const bool diagonal = jb == q, live = m.rev ? jb > q : jb < q;
-            const int c0 = jb * 32;
-            if (diagonal || live) {
-              tmem_ld32(at + c0, v);
-              if (live) {
-                const float away = ex2_ftz(g2 * (float)(m.rev ? c0 - t : t - c0 - 31));
+          for (int c0 = 0; c0 < kTile; c0 += 16) {
+            float v[16], packed[8];
+            const bool live = m.rev ? c0 + 15 >= 32 * q && c0 < n : c0 <= 32 * q + 31;
+            if (live) {
+              tmem_ld16(at + c0, v);
+              // chosen, not multiplied with 0: the rows behind the sequence may hold anything
+              const int end = m.rev ? n - c0 : 16;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float2 x = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), __fmul2_rn(col[j], make_float2(away, away)));
-                  v[2 * j] = x.x, v[2 * j + 1] = x.y;
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  const float d = j & 1 ? diag[j / 2].y : diag[j / 2].x;
-                  v[j] = (m.rev ? j >= lane : j <= lane) ? v[j] * d : 0.f;
-                }
+              for (int j = 0; j < 16; ++j) {
+                const int apart = m.rev ? c0 + j - t : t - c0 - j;
+                v[j] = apart >= 0 && j < end ? v[j] * powers[apart & 127] : 0.f;
               }
-              if (m.rev && c0 + 32 > n) {
-                // chosen, not multiplied with 0: the rows behind the sequence may hold anything
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = c0 + j < n ? v[j] : 0.f;
-              }
+              for (int j = 0; j < 8; ++j) packed[j] = __uint_as_float(pack_bf16(v[2 * j], v[2 * j + 1]));
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+              for (int j = 0; j < 8; ++j) packed[j] = 0.f;
             }
-            // two numbers to a column: block jb's 16 columns lie where scores of blocks already read were
-            float packed[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) packed[j] = __uint_as_float(pack_bf16(v[2 * j], v[2 * j + 1]));
-            tmem_st16(at + jb * 16, packed);
+            // two numbers to a column: they lie where scores already read were
+            tmem_st8(at + c0 / 2, packed);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -373,17 +394,25 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     const int t = threadIdx.x - 256, q = t >> 5;
     const uint32_t row_base = tmem_addr(tmem, q * 32, 0);
     Ring r;
-    uint32_t outs = 0, updates = 0;
+    uint32_t outs = 0, updates = 0, units = 0;
+    const CUtensorMap *out_map = p.outs + which;
+    const bool rev = m.rev;
     // the result that is to be written next
-    __nv_bfloat16 *dst = nullptr;
-    float read = 0.f;
-    bool due = false, mine = false;
+    struct {
+      int row, head, n;
+      uint32_t slot;
+      float read;
+    } due{0, 0, -1, 0, 0.f};
+    int leaving = -1;
     auto write = [&]() {
-      if (!due) return;
-      due = false;
+      if (due.n < 0) return;
       wait(done, outs & 1);
       ++outs;
       tc_fence_after();
+      const bool whole_tile = due.n == kTile;
+      // a's rows are not needed any more: a whole tile goes there, and by TMA to memory, 32 rows from each warp
+      const uint32_t stage = slots + due.slot * C::kSlot;
+      __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(m.out) + ((long long)due.row + t) * m.out_row + (long long)due.head * D;
 #pragma unroll 1
       for (int x = 0; x < D; x += 16) {
         float v[16], u[16];
@@ -391,62 +420,108 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         uint32_t h[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          h[j] = pack_bf16(fmaf(v[2 * j], read, m.within * u[2 * j]), fmaf(v[2 * j + 1], read, m.within * u[2 * j + 1]));
-        if (mine) {
+          h[j] = pack_bf16(fmaf(v[2 * j], due.read, m.within * u[2 * j]), fmaf(v[2 * j + 1], due.read, m.within * u[2 * j + 1]));
+        if (whole_tile) {
+          st_shared_v4(stage + sw128_offset(t, x, kTile), h[0], h[1], h[2], h[3]);
+          st_shared_v4(stage + sw128_offset(t, x + 8, kTile), h[4], h[5], h[6], h[7]);
+        } else if (t < due.n) {
           *reinterpret_cast<uint4 *>(dst + x) = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
       tc_fence_before();
+      if (whole_tile) fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(taken);
+      if (lane == 0) {
+        mbar_arrive(taken);
+        if (whole_tile) {
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            tma_store_3d(out_map, generic + due.slot * C::kSlot + x * 16384 + q * 4096, x * 64, due.head, due.row + 32 * q);
+          tma_store_commit();
+          leaving = (int)due.slot;
+        } else {
+          mbar_arrive(empty + due.slot);
+        }
+      }
+      __syncwarp();
+      due.n = -1;
+    };
+    // The slot from which the last tile is stored, given back as late as the ring allows: a store waits its turn
+    // among the loads.
+    auto give_back = [&]() {
+      if (leaving >= 0) {
+        tma_store_wait_read();
+        mbar_arrive(empty + leaving);
+        leaving = -1;
+      }
     };
     while (walk.next(w, pc)) {
       if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
       const float g2 = log2_decay(p.log_decay, pc.head);
+      const float up = exp2f(g2 * (float)(t + 1)), down_whole = exp2f(g2 * (float)(kTile - 1 - t));
       for (int k = 0; k < pc.t1 - pc.t0; ++k) {
-        const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
+        const int tile = rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
         // rows past n are neither weighed nor written
-        const float up = exp2f(g2 * (float)(t + 1)), down = exp2f(g2 * (float)(n - 1 - t)), weight = m.add * (m.rev ? up : down);
-        for (int g = 0; g < groups; ++g) {
-          uint32_t at[3] = {0, 0, 0}, phase[3] = {0, 0, 0};
+        const float down = n == kTile ? down_whole : exp2f(g2 * (float)(n - 1 - t)), weight = m.add * (rev ? up : down);
+        for (int g = 0; g < groups; ++g, ++units) {
+          uint32_t at[3] = {0, 0, 0};
 #pragma unroll
           for (int o = 0; o < 3; ++o) {
             if (o == 1 && total) continue;
             at[o] = r.slot;
-            phase[o] = r.phase;
             r.next(C::kSlots);
           }
           const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
-          wait(full + at[0], phase[0]);
+          const bool writes = !total && (!sums || g == groups - 1);
+          if (C::kInPlace) {  // five slots: this unit's b waits for it
+            if (lane == 0) give_back();
+            __syncwarp();
+          }
+          wait(full + units % kUnits, (units / kUnits) & 1);
+          if (C::kInPlace && !total) wait(scored, units & 1);  // the scores have read b
           if (sums || g == groups - 1) {
-            const uint32_t high = weighted + (updates % C::kBuffers) * C::kWeighted, rest = high + C::kSlot;
+            const uint32_t rest = weighted + (updates % C::kBuffers) * C::kWeighted + (C::kInPlace ? 0 : C::kSlot),
+                           high = C::kInPlace ? b : rest - C::kSlot;
             if (updates >= C::kBuffers) wait(added + updates % C::kBuffers, (updates / C::kBuffers + 1) & 1);
             ++updates;
-#pragma unroll 2
-            for (int x = 0; x < D; x += 8) {
-              float v[8], lo[8];
-              const uint32_t off = sw128_offset(t, x, kTile);
-              if (t < n) {
-                ld_bf16x8(b + off, v);
-                uint32_t h[4];
+            // a row's sixteen-byte pieces lie at their place in the row's 128 bytes, exclusive-or the row's place in eight
+            const uint32_t at_row = (uint32_t)(t >> 3) * 1024u + (uint32_t)(t & 7) * 128u, swap = (uint32_t)(t & 7) << 4;
+            if (t < n) {
+              // two pieces of eight columns at a time, their loads ahead of the arithmetic
+#pragma unroll 1
+              for (int x = 0; x < D / 8; x += 2) {
+                const uint32_t half = at_row + (uint32_t)(x >> 3) * (kTile * 128u);
+                uint32_t off[2], raw[8], h[8], l[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float v0 = v[2 * j] * weight, v1 = v[2 * j + 1] * weight;
-                  h[j] = pack_bf16(v0, v1);
-                  lo[2 * j] = v0 - __uint_as_float(h[j] << 16);
-                  lo[2 * j + 1] = v1 - __uint_as_float(h[j] & 0xffff0000u);
+                for (int i = 0; i < 2; ++i) {
+                  off[i] = half + ((uint32_t)(((x & 7) + i) << 4) ^ swap);
+                  ld_shared_v4(b + off[i], raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
                 }
-                st_shared_v4(high + off, h[0], h[1], h[2], h[3]);
-                st_bf16x8(rest + off, lo);
-              } else {
-                st_shared_v4(high + off, 0, 0, 0, 0);
-                st_shared_v4(rest + off, 0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(raw[j] << 16), __uint_as_float(raw[j] & 0xffff0000u)),
+                                              make_float2(weight, weight));
+                  h[j] = pack_bf16(v.x, v.y);
+                  // v - h, exactly
+                  const float2 r2 = __ffma2_rn(make_float2(__uint_as_float(h[j] << 16), __uint_as_float(h[j] & 0xffff0000u)),
+                                               make_float2(-1.f, -1.f), v);
+                  l[j] = pack_bf16(r2.x, r2.y);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  st_shared_v4(high + off[i], h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                  st_shared_v4(rest + off[i], l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+                }
+              }
+            } else {
+#pragma unroll 1
+              for (int x = 0; x < D; x += 8) {
+                st_shared_v4(high + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+                st_shared_v4(rest + sw128_offset(t, x, kTile), 0, 0, 0, 0);
               }
             }
           }
-          if (!total) wait(full + at[1], phase[1]);
-          wait(full + at[2], phase[2]);
           if (t >= n) {
             // rows behind the sequence: 0 times whatever they hold has to be 0
 #pragma unroll 1
@@ -454,27 +529,28 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           }
           fence_async_smem();
           named_barrier_sync(2, 128);
-          if (t == 0) {
-#pragma unroll
-            for (int o = 0; o < 3; ++o) {
-              if (o == 1 && total) continue;
-              mbar_arrive(turned + at[o]);  // every slot's, so that its phases go with the loads'
-              mbar_arrive(empty + at[o]);
-            }
+          if (t == 0) mbar_arrive(turned + units % kUnits);
+          if (lane == 0) {
+            mbar_arrive(empty + at[0]);
+            if (!total && !writes) mbar_arrive(empty + at[1]);
+            mbar_arrive(empty + at[2]);
+            if (!C::kInPlace) give_back();
           }
           // the last unit's result, while the MMAs take what was handed out
           write();
-          due = !total && (!sums || g == groups - 1);
-          if (due) {
-            dst = static_cast<__nv_bfloat16 *>(m.out) + ((long long)pc.row0 + tile * kTile + t) * m.out_row +
-                  (long long)(pc.head * m.a_heads + (sums ? 0 : g)) * D;
-            read = m.read * (m.rev ? down : up);
-            mine = t < n;
+          if (writes) {
+            due.row = pc.row0 + tile * kTile;
+            due.head = pc.head * m.a_heads + (sums ? 0 : g);
+            due.n = n;
+            due.slot = at[1];
+            due.read = m.read * (rev ? down : up);
           }
         }
       }
     }
     write();
+    give_back();
+    tma_store_wait_all();  // what this thread has stored leaves shared memory before the block does
   } else {
     // ---- the state -----------------------------------------------------------------
     // Thread t has row t of it (D = 128), or half of row t % 64: with D = 64
@@ -567,7 +643,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
   }
   __syncthreads();
   if (*abort && threadIdx.x == 0)  // copies still on their way land before the block leaves
-    for (int i = 0; i < C::kSlots; ++i)
+    for (int i = 0; i < kUnits; ++i)
       for (uint32_t parity = 0; parity < 2; ++parity) mbar_drain(full + i, parity, 20000000ull);
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
@@ -580,13 +656,13 @@ template <int D> cudaError_t launch(const Args &a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// [tokens][heads][D], rows `row` elements apart; boxes of 128 rows and 64 columns of one head.
-bool make_map(CUtensorMap *map, const void *p, int tokens, long long heads, int d, long long row) {
+// [tokens][heads][D], rows `row` elements apart; boxes of `rows` rows and 64 columns of one head.
+bool make_map(CUtensorMap *map, const void *p, int tokens, long long heads, int d, long long row, int rows) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)row * 2};
-  const cuuint32_t box[3] = {64, 1, kTile};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -620,7 +696,7 @@ cudaError_t mix_tc(const Launch &l, int *status, cudaStream_t st) {
   auto map_of = [&](const void *p, int heads, long long row, int d) -> int {
     for (int i = 0; i < used; ++i)
       if (seen[i].p == p && seen[i].heads == heads && seen[i].row == row) return i;
-    if (used == 4 || !make_map(a.maps + used, p, l.work.tokens, (long long)heads * l.work.heads, d, row)) return -1;
+    if (used == 4 || !make_map(a.maps + used, p, l.work.tokens, (long long)heads * l.work.heads, d, row, kTile)) return -1;
     seen[used] = {p, heads, row};
     return used++;
   };
@@ -630,6 +706,8 @@ cudaError_t mix_tc(const Launch &l, int *status, cudaStream_t st) {
     a.b[i] = (signed char)map_of(m.b, m.b_heads, m.b_row, m.x);
     a.c[i] = (signed char)map_of(m.c, m.b_heads, m.c_row, m.x);
     if (a.a[i] < 0 || a.b[i] < 0 || a.c[i] < 0) return cudaErrorInvalidValue;
+    if (!m.totals && !make_map(a.outs + i, m.out, l.work.tokens, (long long)m.a_heads * l.work.heads, m.y, m.out_row, 32))
+      return cudaErrorInvalidValue;
   }
   for (int i = used; i < 4; ++i) a.maps[i] = a.maps[0];
   return l.mix[0].x == 64 ? launch<64>(a, st) : launch<128>(a, st);
