@@ -41,17 +41,17 @@ using q8::regs_inc;
 
 constexpr int kTile = 128, kThreads = 512;
 constexpr uint32_t kGiveUp = 1u << 21;  // tries of a wait, each of which may sleep for a while: a second or more
-constexpr int kUnits = 4;  // barriers of units in a row: more than the ring holds
+constexpr int kUnits = 16;  // barriers of units in a row: more than the ring holds
 
 template <int D> struct Cfg {
   static constexpr uint32_t kSlot = kTile * D * 2;     // a tile of one operand
-  static constexpr int kSlots = D == 64 ? 8 : 5;
+  static constexpr int kSlots = D == 64 ? 9 : 5;
   static constexpr int kBuffers = D == 64 ? 2 : 1;     // of scores, b~, X and updates
-  static constexpr bool kInPlace = D == 128;           // high parts of b~ take b's place, when the scores are done
-  static constexpr uint32_t kWeighted = kInPlace ? kSlot : 2 * kSlot;  // b~: (high parts and) remainders
+  static constexpr uint32_t kRest = kSlot;             // b~: remainders; its high parts take b's place
   static constexpr uint32_t kState = D * D * 2;
   static constexpr uint32_t kExchange = D == 64 ? 16384 : 0;
-  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kBuffers * (kWeighted + kState) + kExchange + 1024;
+  static constexpr uint32_t kStage = D == 64 ? kSlot : 0;  // results on their way out; at D = 128 in a's slot
+  static constexpr uint32_t kBytes = 1024 + kSlots * kSlot + kBuffers * (kRest + kState) + kExchange + kStage + 1024;
   // tensor memory columns
   static constexpr uint32_t tScores = 0, tRead = 128 * kBuffers, tWithin = tRead + D, tUpdate = tWithin + D;
   static_assert(tUpdate + kBuffers * D <= 512, "tensor memory");
@@ -75,19 +75,24 @@ struct Ring {
   }
 };
 
+// An MN-major operand's descriptor with another distance between its blocks of 64 columns.
+__device__ __forceinline__ uint64_t with_lbo(uint64_t desc, uint32_t bytes) {
+  return (desc & ~((uint64_t)0x3FFF << 16)) | (uint64_t)((bytes >> 4) & 0x3FFF) << 16;
+}
+
 template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ Args p) {
   using C = Cfg<D>;
   extern __shared__ char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   char *generic = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t slots = base, weighted = slots + C::kSlots * C::kSlot, state = weighted + C::kBuffers * C::kWeighted,
-                 exchange = state + C::kBuffers * C::kState;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(generic + (exchange - base) + C::kExchange);
+  const uint32_t slots = base, weighted = slots + C::kSlots * C::kSlot, state = weighted + C::kBuffers * C::kRest,
+                 exchange = state + C::kBuffers * C::kState, stage_at = exchange + C::kExchange, bars_at = stage_at + C::kStage;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(generic + (bars_at - base));
   uint64_t *full = bars, *turned = full + kUnits, *empty = turned + kUnits, *scored = empty + C::kSlots,
            *ready = scored + 2, *done = ready + 2, *taken = done + 1, *added = taken + 1, *whole = added + 2, *known = whole + 2, *drain = known + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  float *powers = reinterpret_cast<float *>(generic + (exchange - base) + C::kExchange + 512);  // lambda^0 .. lambda^127
+  float *powers = reinterpret_cast<float *>(generic + (bars_at - base) + 512);  // lambda^0 .. lambda^127
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
   const int part = blockIdx.x / p.mixes, which = blockIdx.x - part * p.mixes;
@@ -140,13 +145,31 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     return true;
   };
 
+  // A group's heads share b and c, or in reverse a.  These are loaded with the first head and held to the last, where
+  // all the tile's loads fit into the ring; slots are taken in turn, so that a load must not wait for one that is held.
+  // (Without a stage a's slot is held on, until the next tile's first unit has come.)
+  const bool share = (sums ? 2 * groups + (C::kStage ? 1 : 3) : groups + 2) <= C::kSlots;
+  auto loads_bc = [&](int g) { return sums || g == 0 || !share; };
+  auto loads_a = [&](int g) { return !total && (!sums || g == 0 || !share); };
+  auto ends_bc = [&](int g) { return sums || g == groups - 1 || !share; };
+  auto ends_a = [&](int g) { return !sums || g == groups - 1 || !share; };
+  // A unit's slots, as the ring gives them.
+  struct Unit {
+    uint32_t b, a, c;
+  };
+  auto advance = [&](Unit &u, Ring &r, int g) {
+    if (loads_bc(g)) u.b = r.slot, r.next(C::kSlots);
+    if (loads_a(g)) u.a = r.slot, r.next(C::kSlots);
+    if (loads_bc(g)) u.c = r.slot, r.next(C::kSlots);
+  };
+
   Walk walk(w, part, m.rev);
   Piece pc;
   if (wg == 0) {
     regs_dec<96>();
     if (warp == 0) {
       // ---- loads: b, a, c of each unit -------------------------------------------
-      const CUtensorMap *maps[3] = {p.maps + p.b[which], p.maps + (total ? 0 : p.a[which]), p.maps + p.c[which]};
+      const CUtensorMap *map_b = p.maps + p.b[which], *map_a = p.maps + (total ? 0 : p.a[which]), *map_c = p.maps + p.c[which];
       const int b_heads = m.b_heads, a_heads = m.a_heads;
       Ring r;
       uint32_t unit = 0;
@@ -157,14 +180,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           for (int g = 0; g < groups; ++g, ++unit) {
             uint64_t *bar = full + unit % kUnits;
             const int hb = pc.head * b_heads + (b_heads > 1 ? g : 0), ha = pc.head * a_heads + (a_heads > 1 ? g : 0);
-#pragma unroll
+            const bool bc = loads_bc(g), na = loads_a(g);
+            if (!total && !(bc && na) && elect_lane()) mbar_arrive_n(bar, na ? 2 : 1);
+#pragma unroll 1
             for (int o = 0; o < 3; ++o) {
-              if (o == 1 && total) continue;
+              if (o == 1 ? !na : !bc) continue;
               const bool ok = __all_sync(0xffffffffu, wait(empty + r.slot, r.phase ^ 1));
               if (ok && elect_lane()) {
+                const CUtensorMap *map = o == 0 ? map_b : o == 1 ? map_a : map_c;
                 mbar_arrive_expect_tx(bar, C::kSlot);
                 for (int x = 0; x < D / 64; ++x)
-                  tma_load_3d(generic + r.slot * C::kSlot + x * 16384, maps[o], bar, x * 64, o == 1 ? ha : hb, row);
+                  tma_load_3d(generic + r.slot * C::kSlot + x * 16384, map, bar, x * 64, o == 1 ? ha : hb, row);
               }
               __syncwarp();
               r.next(C::kSlots);
@@ -180,33 +206,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       // registers.  Formed by the issuing lane alone they took three times as long as the MMAs.
       const bool issues = elect_lane();
       const uint64_t rows_k = desc_kmajor(slots, kTile, 0, 0), rows_mn = desc_mnmajor(slots, kTile, 0, 0),
-                     weighted_mn = desc_mnmajor(weighted, kTile, 0, 0), state_mn = desc_mnmajor(state, D, 0, 0);
+                     rest_mn = desc_mnmajor(weighted, kTile, 0, 0), state_mn = desc_mnmajor(state, D, 0, 0);
       constexpr uint32_t kSlotStep = C::kSlot >> 4;
       const uint32_t id_scores = make_idesc(128, 128, false, false), id_state = make_idesc(128, D, false, true),
                      id_update = make_idesc(128, D, true, true);
       bool alive = true;
       auto agree = [&](bool ok) { alive = alive && __all_sync(0xffffffffu, ok); };
-      // A unit's slots, as the ring gives them: b, a, c (b, c).
-      struct Unit {
-        uint32_t b, a, c;
-      };
-      auto unit_at = [&](Ring &t) {
-        Unit u{};
-        u.b = t.slot;
-        t.next(C::kSlots);
-        if (!total) {
-          u.a = t.slot;
-          t.next(C::kSlots);
-        }
-        u.c = t.slot;
-        t.next(C::kSlots);
-        return u;
-      };
       Ring r;
       uint32_t unit = 0, outs = 0, tiles = 0, updates = 0;
       if (warp == 1 && !total) {
         uint32_t scored_units = 0;
-        auto scores = [&](const Unit &u) {
+        auto scores = [&](const Unit &u, bool release) {
           const uint32_t buffer = scored_units++ % C::kBuffers, d = tmem + C::tScores + buffer * 128;
           if (!alive) return;
           tc_fence_after();
@@ -217,7 +227,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             if (issues) mma_bf16(d, a + at, b + at, id_scores, s > 0);
           }
           if (issues) mma_commit(scored + buffer);
-          if (issues) mma_commit(empty + u.b);
+          if (release && issues) mma_commit(empty + u.b);
           __syncwarp();
         };
         Unit now{}, then{};
@@ -231,24 +241,27 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                 now = then;
                 ahead = false;
               } else {
-                now = unit_at(r);
+                advance(now, r, g);
                 agree(wait(full + unit % kUnits, (unit / kUnits) & 1));
-                scores(now);
+                scores(now, ends_bc(g));
               }
-              // the scores of the next unit, if its rows are here: whether there is a next one shows in the barrier
-              // alone, which completes no phase without loads
+              // The scores of the next unit, as soon as its rows are here and until this one's are weighed: whether
+              // there is a next one shows in the barrier alone, which completes no phase without loads.
+              const uint32_t buffer = unit % C::kBuffers;
               if (C::kBuffers == 2) {
-                Ring t = r;
-                const Unit u = unit_at(t);
-                const bool here = mbar_test(full + (unit + 1) % kUnits, ((unit + 1) / kUnits) & 1);
-                if (__all_sync(0xffffffffu, here) && alive) {
-                  then = u;
-                  r = t;
-                  ahead = true;
-                  scores(u);
+                const uint32_t then_unit = unit + 1;
+#pragma unroll 1
+                for (int i = 0; i < 4096 && alive; ++i) {
+                  if (__all_sync(0xffffffffu, mbar_test(full + then_unit % kUnits, (then_unit / kUnits) & 1))) {
+                    then = now;
+                    advance(then, r, last ? 0 : g + 1);
+                    ahead = true;
+                    scores(then, ends_bc(last ? 0 : g + 1));
+                    break;
+                  }
+                  if (__all_sync(0xffffffffu, mbar_test(ready + buffer, (unit / C::kBuffers) & 1))) break;
                 }
               }
-              const uint32_t buffer = unit % C::kBuffers;
               agree(wait(turned + unit % kUnits, (unit / kUnits) & 1));
               agree(wait(ready + buffer, (unit / C::kBuffers) & 1));
               if (g == 0 || !sums) agree(wait(taken, (outs & 1) ^ 1));
@@ -260,8 +273,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                 for (int s = 0; s < 8; ++s)
                   if (issues)
                     mma_bf16_ta(tmem + C::tWithin, tmem + C::tScores + buffer * 128 + s * 8, c + s * 128u, id_state, s > 0 || !first);
-                if (issues) mma_commit(empty + now.a);
-                if (issues) mma_commit(empty + now.c);
+                if (ends_a(g) && issues) mma_commit(empty + now.a);
+                if (ends_bc(g) && issues) mma_commit(empty + now.c);
                 if ((last || !sums) && issues) mma_commit(done);
                 __syncwarp();
               }
@@ -270,12 +283,13 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           }
         }
       } else if (warp == 2) {
+        Unit now{};
         while (walk.next(w, pc)) {
           if ((total && !piece_has_total(m, pc)) || pc.rows == 0) continue;
           for (int k = 0; k < pc.t1 - pc.t0; ++k, ++tiles) {
             for (int g = 0; g < groups; ++g, ++unit) {
               const bool last = g == groups - 1, update = sums || last;
-              const Unit now = unit_at(r);
+              advance(now, r, g);
               uint64_t *bar = full + unit % kUnits;
               const uint32_t phase = (unit / kUnits) & 1;
               auto read = [&]() {
@@ -296,7 +310,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                     if (issues) mma_commit(done);
                   }
                 }
-                if (alive && issues) mma_commit(empty + now.a);
+                if (ends_a(g) && alive && issues) mma_commit(empty + now.a);
                 __syncwarp();
               };
               // with two buffers the update goes first, ahead of the state that this tile reads; with one it would
@@ -309,11 +323,14 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                 if (update) {
                   const bool first = !sums || g == 0;
                   const uint32_t d = tmem + C::tUpdate + (tiles % C::kBuffers) * D;
-                  const uint64_t c = rows_mn + now.c * kSlotStep, rest = weighted_mn + (updates % C::kBuffers) * (C::kWeighted >> 4),
-                                 high = C::kInPlace ? rows_mn + now.b * kSlotStep : rest;
+                  const uint64_t c = rows_mn + now.c * kSlotStep, rest = rest_mn + (updates % C::kBuffers) * (C::kRest >> 4),
+                                 high = rows_mn + now.b * kSlotStep;
+                  // At D = 64 high parts and remainders are one operand of 128 columns, so that one MMA takes both:
+                  // its columns 64 to 127 lie as far behind the first as the remainders behind b's slot.
+                  const uint64_t both = D == 64 ? with_lbo(high, weighted + (updates % C::kBuffers) * C::kRest - (slots + now.b * C::kSlot)) : high;
 #pragma unroll
                   for (int s = 0; s < 8; ++s)
-                    if (issues) mma_bf16(d, high + s * 128u, c + s * 128u, id_update, s > 0 || !first);
+                    if (issues) mma_bf16(d, both + s * 128u, c + s * 128u, id_update, s > 0 || !first);
                   if constexpr (D == 128) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
@@ -322,8 +339,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
                   if (issues) mma_commit(added + updates % C::kBuffers);
                   if (last && issues) mma_commit(whole + tiles % C::kBuffers);
                 }
-                if (issues) mma_commit(empty + now.b);
-                if (issues) mma_commit(empty + now.c);
+                if (ends_bc(g) && issues) mma_commit(empty + now.b);
+                if (ends_bc(g) && issues) mma_commit(empty + now.c);
                 __syncwarp();
               }
               if (update) ++updates;
@@ -394,6 +411,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     const int t = threadIdx.x - 256, q = t >> 5;
     const uint32_t row_base = tmem_addr(tmem, q * 32, 0);
     Ring r;
+    Unit now{};
     uint32_t outs = 0, updates = 0, units = 0;
     const CUtensorMap *out_map = p.outs + which;
     const bool rev = m.rev;
@@ -410,8 +428,13 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       ++outs;
       tc_fence_after();
       const bool whole_tile = due.n == kTile;
-      // a's rows are not needed any more: a whole tile goes there, and by TMA to memory, 32 rows from each warp
-      const uint32_t stage = slots + due.slot * C::kSlot;
+      // a whole tile goes by TMA, 32 rows from each warp: from a place of its own, or at D = 128 from a's slot, whose
+      // rows are not needed any more
+      const uint32_t stage = C::kStage ? stage_at : slots + due.slot * C::kSlot;
+      if (C::kStage) {
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+      }
       __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(m.out) + ((long long)due.row + t) * m.out_row + (long long)due.head * D;
 #pragma unroll 1
       for (int x = 0; x < D; x += 16) {
@@ -437,10 +460,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         if (whole_tile) {
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
-            tma_store_3d(out_map, generic + due.slot * C::kSlot + x * 16384 + q * 4096, x * 64, due.head, due.row + 32 * q);
+            tma_store_3d(out_map, generic + (stage - base) + x * 16384 + q * 4096, x * 64, due.head, due.row + 32 * q);
           tma_store_commit();
-          leaving = (int)due.slot;
-        } else {
+          leaving = C::kStage ? -1 : (int)due.slot;
+        } else if (!C::kStage) {
           mbar_arrive(empty + due.slot);
         }
       }
@@ -465,24 +488,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         // rows past n are neither weighed nor written
         const float down = n == kTile ? down_whole : exp2f(g2 * (float)(n - 1 - t)), weight = m.add * (rev ? up : down);
         for (int g = 0; g < groups; ++g, ++units) {
-          uint32_t at[3] = {0, 0, 0};
-#pragma unroll
-          for (int o = 0; o < 3; ++o) {
-            if (o == 1 && total) continue;
-            at[o] = r.slot;
-            r.next(C::kSlots);
-          }
-          const uint32_t b = slots + at[0] * C::kSlot, c = slots + at[2] * C::kSlot;
-          const bool writes = !total && (!sums || g == groups - 1);
-          if (C::kInPlace) {  // five slots: this unit's b waits for it
+          advance(now, r, g);
+          const uint32_t b = slots + now.b * C::kSlot, c = slots + now.c * C::kSlot;
+          const bool writes = !total && (!sums || g == groups - 1), update = sums || g == groups - 1;
+          if (C::kStage == 0) {  // the ring is short: this unit's b may wait for it
             if (lane == 0) give_back();
             __syncwarp();
           }
           wait(full + units % kUnits, (units / kUnits) & 1);
-          if (C::kInPlace && !total) wait(scored, units & 1);  // the scores have read b
-          if (sums || g == groups - 1) {
-            const uint32_t rest = weighted + (updates % C::kBuffers) * C::kWeighted + (C::kInPlace ? 0 : C::kSlot),
-                           high = C::kInPlace ? b : rest - C::kSlot;
+          if (!total) wait(scored + units % C::kBuffers, (units / C::kBuffers) & 1);  // the scores have read b
+          if (update) {
+            const uint32_t rest = weighted + (updates % C::kBuffers) * C::kRest, high = b;
             if (updates >= C::kBuffers) wait(added + updates % C::kBuffers, (updates / C::kBuffers + 1) & 1);
             ++updates;
             // a row's sixteen-byte pieces lie at their place in the row's 128 bytes, exclusive-or the row's place in eight
@@ -522,19 +538,20 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
               }
             }
           }
-          if (t >= n) {
+          if (loads_bc(g) && t >= n) {
             // rows behind the sequence: 0 times whatever they hold has to be 0
 #pragma unroll 1
             for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
           }
-          fence_async_smem();
-          named_barrier_sync(2, 128);
+          if (update || n < kTile) {
+            fence_async_smem();
+            named_barrier_sync(2, 128);
+          }
           if (t == 0) mbar_arrive(turned + units % kUnits);
           if (lane == 0) {
-            mbar_arrive(empty + at[0]);
-            if (!total && !writes) mbar_arrive(empty + at[1]);
-            mbar_arrive(empty + at[2]);
-            if (!C::kInPlace) give_back();
+            if (ends_bc(g)) mbar_arrive(empty + now.b);
+            if (!total && ends_a(g) && (C::kStage || !writes)) mbar_arrive(empty + now.a);
+            if (ends_bc(g)) mbar_arrive(empty + now.c);
           }
           // the last unit's result, while the MMAs take what was handed out
           write();
@@ -542,7 +559,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             due.row = pc.row0 + tile * kTile;
             due.head = pc.head * m.a_heads + (sums ? 0 : g);
             due.n = n;
-            due.slot = at[1];
+            due.slot = now.a;
             due.read = m.read * (rev ? down : up);
           }
         }
