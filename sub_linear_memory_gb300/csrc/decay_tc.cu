@@ -360,6 +360,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     // ---- weighted scores: thread t has row t -------------------------------------
     const int t = threadIdx.x - 128, q = t >> 5;
     const uint32_t row_base = tmem_addr(tmem, q * 32, C::tScores);
+    const bool rev = m.rev;
     uint32_t unit = 0;
     while (walk.next(w, pc)) {
       if (total || pc.rows == 0) continue;
@@ -367,36 +368,49 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       named_barrier_sync(3, 128);
       powers[t] = exp2f(g2 * (float)t);
       named_barrier_sync(3, 128);
+      float2 col[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) col[j] = make_float2(powers[rev ? 2 * j : 31 - 2 * j], powers[rev ? 2 * j + 1 : 30 - 2 * j]);
       for (int k = 0; k < pc.t1 - pc.t0; ++k) {
         const int tile = m.rev ? pc.t1 - 1 - k : pc.t0 + k, n = min(kTile, pc.rows - tile * kTile);
         for (int g = 0; g < groups; ++g, ++unit) {
           const uint32_t sb = unit % C::kBuffers, at = row_base + sb * 128;
           wait(scored + sb, (unit / C::kBuffers) & 1);
           tc_fence_after();
-          // Sixteen columns at a time: a warp's rows have consecutive powers in a column.  Rolled: unrolled, and with
-          // powers in registers, the block's code was past the instruction caches, and everything in it three times
-          // as slow.
+          // 32 columns at a time.  Away from the diagonal the weight is a power to the block's nearer end times a
+          // column's; on it, and where the sequence ends inside a block, each weight comes from the table.  Rolled:
+          // unrolled, the block's code was past the instruction caches, and everything in it three times as slow.
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTile; c0 += 16) {
-            float v[16], packed[8];
-            const bool live = m.rev ? c0 + 15 >= 32 * q && c0 < n : c0 <= 32 * q + 31;
+          for (int c0 = 0; c0 < kTile; c0 += 32) {
+            float v[32];
+            const bool live = rev ? c0 >= 32 * q && c0 < n : c0 <= 32 * q;
             if (live) {
-              tmem_ld16(at + c0, v);
-              // chosen, not multiplied with 0: the rows behind the sequence may hold anything
-              const int end = m.rev ? n - c0 : 16;
+              tmem_ld32(at + c0, v);
+              if (c0 != 32 * q && (!rev || c0 + 32 <= n)) {
+                const float away = powers[rev ? c0 - t : t - c0 - 31];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int apart = m.rev ? c0 + j - t : t - c0 - j;
-                v[j] = apart >= 0 && j < end ? v[j] * powers[apart & 127] : 0.f;
+                for (int j = 0; j < 16; ++j) {
+                  const float2 x = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), __fmul2_rn(col[j], make_float2(away, away)));
+                  v[2 * j] = x.x, v[2 * j + 1] = x.y;
+                }
+              } else {
+                // chosen, not multiplied with 0: the rows behind the sequence may hold anything
+                const int end = rev ? n - c0 : 32, off = rev ? c0 - t : t - c0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const int apart = rev ? off + j : off - j;
+                  v[j] = apart >= 0 && j < end ? v[j] * powers[apart & 127] : 0.f;
+                }
               }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) packed[j] = __uint_as_float(pack_bf16(v[2 * j], v[2 * j + 1]));
             } else {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) packed[j] = 0.f;
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
             }
             // two numbers to a column: they lie where scores already read were
-            tmem_st8(at + c0 / 2, packed);
+            float packed[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) packed[j] = __uint_as_float(pack_bf16(v[2 * j], v[2 * j + 1]));
+            tmem_st16(at + c0 / 2, packed);
           }
           tmem_st_wait();
           tc_fence_before();
