@@ -39,12 +39,18 @@ using q8::elect_lane;
 using q8::regs_dec;
 using q8::regs_inc;
 
-constexpr int kTile = 128, kThreads = 512;
+constexpr int kTile = 128;
 constexpr uint32_t kGiveUp = 1u << 21;  // tries of a wait, each of which may sleep for a while: a second or more
 constexpr int kUnits = 16;  // barriers of units in a row: more than the ring holds
 
 template <int D> struct Cfg {
   static constexpr uint32_t kSlot = kTile * D * 2;     // a tile of one operand
+  // At D = 64 a warpgroup of its own writes the results; at 128 the state's registers leave none.  Registers of the
+  // warpgroups (loads and MMAs, weighted scores, rows, results, state): at most 640 x 96 or 512 x 128 in all.
+  static constexpr bool kWriters = D == 64;
+  static constexpr int kThreads = D == 64 ? 640 : 512;
+  static constexpr int kRegs0 = D == 64 ? 88 : 96, kRegsScores = D == 64 ? 112 : 128, kRegsRows = D == 64 ? 72 : 80,
+                       kRegsState = D == 64 ? 120 : 208;
   static constexpr int kSlots = D == 64 ? 9 : 5;
   static constexpr int kBuffers = D == 64 ? 2 : 1;     // of scores, b~, X and updates
   static constexpr uint32_t kRest = kSlot;             // b~: remainders; its high parts take b's place
@@ -80,7 +86,7 @@ __device__ __forceinline__ uint64_t with_lbo(uint64_t desc, uint32_t bytes) {
   return (desc & ~((uint64_t)0x3FFF << 16)) | (uint64_t)((bytes >> 4) & 0x3FFF) << 16;
 }
 
-template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ Args p) {
+template <int D> __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tc_kernel(const __grid_constant__ Args p) {
   using C = Cfg<D>;
   extern __shared__ char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -166,7 +172,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
   Walk walk(w, part, m.rev);
   Piece pc;
   if (wg == 0) {
-    regs_dec<96>();
+    regs_dec<C::kRegs0>();
     if (warp == 0) {
       // ---- loads: b, a, c of each unit -------------------------------------------
       const CUtensorMap *map_b = p.maps + p.b[which], *map_a = p.maps + (total ? 0 : p.a[which]), *map_c = p.maps + p.c[which];
@@ -358,6 +364,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     }
   } else if (wg == 1) {
     // ---- weighted scores: thread t has row t -------------------------------------
+    if (C::kWriters) regs_inc<C::kRegsScores>();
     const int t = threadIdx.x - 128, q = t >> 5;
     const uint32_t row_base = tmem_addr(tmem, q * 32, C::tScores);
     const bool rev = m.rev;
@@ -419,10 +426,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
         }
       }
     }
-  } else if (wg == 2) {
+  } else if (wg == 2 || wg == 4) {
     // ---- rows: thread t has row t, of b to weigh it and of the results to write them ----
-    regs_dec<80>();
-    const int t = threadIdx.x - 256, q = t >> 5;
+    regs_dec<C::kRegsRows>();
+    const int t = threadIdx.x & 127, q = t >> 5;
+    const bool weighs = wg == 2, results = !total && (!C::kWriters || wg == 4);
     const uint32_t row_base = tmem_addr(tmem, q * 32, 0);
     Ring r;
     Unit now{};
@@ -505,6 +513,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
           advance(now, r, g);
           const uint32_t b = slots + now.b * C::kSlot, c = slots + now.c * C::kSlot;
           const bool writes = !total && (!sums || g == groups - 1), update = sums || g == groups - 1;
+          if (weighs) {
           if (C::kStage == 0) {  // the ring is short: this unit's b may wait for it
             if (lane == 0) give_back();
             __syncwarp();
@@ -567,14 +576,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
             if (!total && ends_a(g) && (C::kStage || !writes)) mbar_arrive(empty + now.a);
             if (ends_bc(g)) mbar_arrive(empty + now.c);
           }
-          // the last unit's result, while the MMAs take what was handed out
-          write();
+          }
+          if (!results) continue;
+          // where the rows' warpgroup does both, the last unit's result, while the MMAs take what was handed out
+          if (!C::kWriters) write();
           if (writes) {
             due.row = pc.row0 + tile * kTile;
             due.head = pc.head * m.a_heads + (sums ? 0 : g);
             due.n = n;
             due.slot = now.a;
             due.read = m.read * (rev ? down : up);
+            if (C::kWriters) write();
           }
         }
       }
@@ -587,7 +599,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
     // Thread t has row t of it (D = 128), or half of row t % 64: with D = 64
     // the update's rows 0-63 are those of the high parts and 64-127 those of
     // the remainders, so two threads exchange halves and add.
-    regs_inc<208>();
+    regs_inc<C::kRegsState>();
     constexpr int kOwn = D == 64 ? 32 : 128;
     const int t = threadIdx.x - 384, q = t >> 5;
     const int srow = D == 64 ? t & 63 : t, scol = D == 64 ? (t >> 6) * 32 : 0;
@@ -612,22 +624,21 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
       const uint32_t from = row_base + (summed % C::kBuffers) * D;
       ++summed;
       if constexpr (D == 64) {
-        float u[32], v[32];
-        tmem_ld32x2(from, from + 32, u, v);
-        const bool low = t >= 64;
+        const uint32_t own = t >= 64 ? 32 : 0;
+        float u[32];
+        tmem_ld32(from + (32 - own), u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float *give = low ? u + 4 * i : v + 4 * i;
-          st_shared_v4(exchange + (i * 128 + t) * 16, __float_as_uint(give[0]), __float_as_uint(give[1]),
-                       __float_as_uint(give[2]), __float_as_uint(give[3]));
-        }
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4(exchange + (i * 128 + t) * 16, __float_as_uint(u[4 * i]), __float_as_uint(u[4 * i + 1]),
+                       __float_as_uint(u[4 * i + 2]), __float_as_uint(u[4 * i + 3]));
+        tmem_ld32(from + own, u);
         named_barrier_sync(kBar, 128);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float x[4];
           ld_shared_v4f(exchange + (i * 128 + (t ^ 64)) * 16, x);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[4 * i + j] = fmaf(s[4 * i + j], keep, (low ? v[4 * i + j] : u[4 * i + j]) + x[j]);
+          for (int j = 0; j < 4; ++j) s[4 * i + j] = fmaf(s[4 * i + j], keep, u[4 * i + j] + x[j]);
         }
       } else {
 #pragma unroll
@@ -683,7 +694,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const 
 template <int D> cudaError_t launch(const Args &a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kBytes);
   if (e != cudaSuccess) return e;
-  tc_kernel<D><<<a.work.parts * a.mixes, kThreads, Cfg<D>::kBytes, st>>>(a);
+  tc_kernel<D><<<a.work.parts * a.mixes, Cfg<D>::kThreads, Cfg<D>::kBytes, st>>>(a);
   return cudaGetLastError();
 }
 
