@@ -89,10 +89,9 @@ __device__ __forceinline__ void decode4(uint32_t c, float s, float *v) {
 // |x| 2^-e <= 448 to one of the two codes around it: 20 random bits are added
 // below the three that stay.  Codes below 2^-6 lie as far apart as those from
 // there to 2^-5, so 2^-6 more puts them there.
-__device__ __forceinline__ float round_at_random(float w, uint32_t bits16) {
+__device__ __forceinline__ float round_at_random(float w, uint32_t bits20) {
   const float up = w < 0.015625f ? 0.015625f : 0.f;
-  const float t = __uint_as_float((__float_as_uint(w + up) + (bits16 << 4)) & 0xFFF00000u) - up;
-  return fminf(t, 448.f);
+  return __uint_as_float((__float_as_uint(w + up) + bits20) & 0xFFF00000u) - up;
 }
 
 // The codes of 4 values of a block of 128 (one warp's), and its scale byte.
@@ -107,13 +106,26 @@ __device__ __forceinline__ uint32_t encode4(const float *x, const uint32_t *word
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float a = fabsf(x[i]);
-    float w = round_at_random(a * inv, (words[i] >> shift) & 0xFFFFu);
+    float w = fminf(round_at_random(a * inv, shift ? words[i] >> 12 & 0xFFFF0u : words[i] << 4 & 0xFFFF0u), most);
     if (never_zero && a > 0.f) w = fmaxf(w, 0.001953125f);
-    y[i] = copysignf(fminf(w, most), x[i]);
+    y[i] = copysignf(w, x[i]);
   }
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
+}
+
+// The hardware's root and inverse, within two units: the step's own rounding into p is far larger.  Roots of numbers
+// below fp32's normal range are 0.
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <typename G, bool EIGHT, int MOST>
@@ -124,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const float steps = (float)(o.count[0] + 1), lr = o.lr_now ? *o.lr_now : o.lr;
     // 1 - b^t without the difference's loss
     now[0] = lr / -expm1f(steps * o.log_b1);
-    now[1] = 1.f / -expm1f(steps * o.log_b2);
+    now[1] = rsqrtf(-expm1f(steps * o.log_b2));
     now[2] = 1.f - lr * o.wd;
     now[3] = __int_as_float(o.count[0] + 1);
   }
@@ -162,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     }
   }
   __syncthreads();
-  const float rate = now[0], inv_c2 = now[1], keep = now[2];
+  const float rate = -now[0], root_c2 = now[1], keep = now[2];
   const uint32_t steps = __float_as_uint(now[3]);
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
@@ -173,26 +185,29 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i][j] *= v[i][j];
     }
+    float r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float gv = g[i][j];
       m[i][j] = fmaf(m[i][j], o.b1, gv * (1.f - o.b1));
       v[i][j] = fmaf(v[i][j], o.b2, gv * gv * (1.f - o.b2));
-      p[i][j] = fmaf(p[i][j], keep, -rate * (m[i][j] / (sqrtf(v[i][j] * inv_c2) + o.eps)));
+      r[j] = root(v[i][j]);
+      p[i][j] = fmaf(p[i][j], keep, rate * m[i][j] * inverse(fmaf(r[j], root_c2, o.eps)));
     }
     store4(e.p + at, left, vec_p, p[i]);
     if constexpr (EIGHT) {
       uint32_t w[4] = {(uint32_t)((unsigned long long)at >> 2), (uint32_t)e.index, (uint32_t)((unsigned long long)at >> 34),
                        steps};
       philox4x32_10(w, o.seed0, o.seed1);
-      float r[4], x[4];
+      if (left < 4) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = j < left ? m[i][j] : 0.f;
-        r[j] = j < left ? sqrtf(v[i][j]) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          m[i][j] = j < left ? m[i][j] : 0.f;
+          r[j] = j < left ? r[j] : 0.f;
+        }
       }
       int mb, vb;
-      const uint32_t m4 = encode4(x, w, 0, false, mb), v4 = encode4(r, w, 16, true, vb);
+      const uint32_t m4 = encode4(m[i], w, 0, false, mb), v4 = encode4(r, w, 16, true, vb);
       if (at / q8::kBlock * q8::kBlock < e.n) {
         // past the tensor's end codes stay 0, in a NaN block too
         const uint32_t inside = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;

@@ -33,7 +33,6 @@ struct Work {
   const int *cu;      // [seqs + 1] first rows, or NULL: seqs sequences of `length` rows
   int tokens, seqs, length, heads, tile, parts;
   const int4 *where;  // [parts + 1] (head, sequence, tile, -) of each share, or NULL where it can be computed
-  const long long *tiles;  // with `where`: tiles of one head
 };
 
 // One pass of the operator.
@@ -77,7 +76,7 @@ struct Scan {
 struct Prepare {
   Work work;
   int4 *where;
-  long long *tiles;
+  long long *first;  // [seqs]
   const int *slots;
   int places;
   int *owner, *place;

@@ -85,7 +85,7 @@ bool tc_shape(const slim_decay_shape &s) { return s.dk == s.dv && (s.dk == 64 ||
 
 // The workspace's parts, in bytes from its start.
 struct Layout {
-  size_t where, tiles, owner, place, totals[2], incoming[2], first, bytes;
+  size_t where, first_tile, owner, place, totals[2], incoming[2], first, bytes;
 };
 
 Layout layout(const slim_decay_shape &s, const Cut &c, bool bwd) {
@@ -98,7 +98,7 @@ Layout layout(const slim_decay_shape &s, const Cut &c, bool bwd) {
   };
   const size_t states = c.joined ? sizeof(float) * (size_t)c.parts * s.dk * s.dv : 0;
   l.where = take(sizeof(int4) * (size_t)(c.parts + 1));
-  l.tiles = take(sizeof(long long));
+  l.first_tile = take(sizeof(long long) * (size_t)s.seqs);
   l.owner = take(sizeof(int) * (size_t)s.places);
   l.place = take(sizeof(int) * (size_t)s.seqs);
   for (int i = 0; i < (bwd ? 2 : 1); ++i) {
@@ -127,14 +127,14 @@ slim_status begin(const slim_decay_shape &s, const Cut &c, bool bwd, const int *
   if (!aligned(workspace, 256)) return SLIM_ERR_UNSUPPORTED;
   call.ws = static_cast<char *>(workspace);
   call.joined = c.joined;
-  call.work = Work{cu, s.tokens, s.seqs, cu ? 0 : s.tokens / s.seqs, s.heads, c.tile, c.parts, nullptr, nullptr};
+  call.work = Work{cu, s.tokens, s.seqs, cu ? 0 : s.tokens / s.seqs, s.heads, c.tile, c.parts, nullptr};
   call.place = nullptr;
   const bool listed = cu && s.seqs > 1;
   if (!listed && !slots) return SLIM_OK;
   Prepare p{call.work, nullptr, nullptr, slots, s.places, nullptr, nullptr};
   if (listed) {
     p.where = call.part<int4>(call.at.where);
-    p.tiles = call.part<long long>(call.at.tiles);
+    p.first = call.part<long long>(call.at.first_tile);
   }
   if (slots) {
     p.owner = call.part<int>(call.at.owner);
@@ -143,7 +143,6 @@ slim_status begin(const slim_decay_shape &s, const Cut &c, bool bwd, const int *
   }
   if (prepare(p, st) != cudaSuccess) return SLIM_ERR_CUDA;
   call.work.where = p.where;
-  call.work.tiles = p.tiles;
   return SLIM_OK;
 }
 

@@ -36,9 +36,9 @@ __device__ long long block_exclusive(long long v, long long *warp_sums, long lon
   return before;
 }
 
-// One block: the tiles of all sequences are counted, then a second pass over
-// them finds the shares that begin in each; and each sequence's place in the
-// cache, which the first of the sequences that name it has.
+// One block: the tiles of all sequences are counted, then each share finds
+// the sequence that it begins in; and each sequence's place in the cache,
+// which the first of the sequences that name it has.
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(Prepare p) {
   __shared__ long long warp_sums[32];
   const Work &w = p.work;
@@ -60,27 +60,26 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(Prepare p) {
     }
   }
   if (!p.where) return;
+  // first[i]: the tiles before sequence i, in shared memory where they fit
+  __shared__ long long near[kPrepThreads];
+  long long *first = w.seqs <= kPrepThreads ? near : p.first;
   long long tiles = 0;
-  for (int i = 0; i < w.seqs; i += kPrepThreads)
-    block_exclusive(i + t < w.seqs ? tiles_of(w, bounds(w, i + t).y) : 0, warp_sums, tiles);
-  const long long all = tiles * w.heads;
-  if (t == 0) {
-    *p.tiles = tiles;
-    p.where[w.parts] = make_int4(w.heads, 0, 0, 0);
-  }
-  long long carry = 0;
   for (int i = 0; i < w.seqs; i += kPrepThreads) {
-    const int n = i + t < w.seqs ? tiles_of(w, bounds(w, i + t).y) : 0;
-    const long long first = block_exclusive(n, warp_sums, carry);
-    for (int h = 0; h < w.heads && n > 0; ++h) {
-      // shares whose first tile f = floor(all c / parts) lies in [at, at + n)
-      const long long at = h * tiles + first;
-      for (long long c = (at * w.parts + all - 1) / all; c < w.parts; ++c) {
-        const long long f = all * c / w.parts;
-        if (f >= at + n) break;
-        if (f >= at) p.where[c] = make_int4(h, i + t, (int)(f - at), 0);
-      }
+    const long long before = block_exclusive(i + t < w.seqs ? tiles_of(w, bounds(w, i + t).y) : 0, warp_sums, tiles);
+    if (i + t < w.seqs) first[i + t] = before;
+  }
+  __syncthreads();
+  const long long all = tiles * w.heads;
+  for (int c = t; c <= w.parts; c += kPrepThreads) {
+    const long long f = all * c / w.parts;
+    const int head = (int)(f / tiles);
+    const long long r = f - head * tiles;
+    int lo = 0, hi = head < w.heads ? w.seqs - 1 : 0;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= r) lo = mid; else hi = mid - 1;
     }
+    p.where[c] = make_int4(head, lo, head < w.heads ? (int)(r - first[lo]) : 0, 0);
   }
 }
 
@@ -110,16 +109,42 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
   float x = at >= 0 && live ? side.start[((size_t)at * w.heads + edge.head) * s.states + e] : 0.f;
   if (live && side.first) side.first[(size_t)c * s.states + e] = x;
   int from = side.rev ? b.y : 0;  // rows already passed lie before (behind) this one
-  Place border = edge;
+  // The sequence's next shares, a block's threads' worth at a time: where each ends, from all threads at once; then
+  // along them with eight totals on their way.
+  __shared__ int rows[kScanThreads + 1];
   while (true) {
-    const int to = border.tile * w.tile;
-    const float keep = exp2f(g * (float)abs(to - from));
-    if (live && to != from) x = fmaf(x, keep, side.totals[(size_t)c * s.states + e]);  // a share may be empty
-    c += step;
-    if (live) side.incoming[(size_t)c * s.states + e] = x;
-    from = to;
-    border = share_begin(w, side.rev ? c : c + 1);
-    if (border.head != edge.head || border.seq != edge.seq || border.tile == 0) return;
+    const int next = side.rev ? c + step * (int)threadIdx.x : c + 1 + (int)threadIdx.x;
+    int to = -1;  // behind the sequence
+    if (next >= 0 && next <= w.parts) {
+      const Place q = share_begin(w, next);
+      if (q.head == edge.head && q.seq == edge.seq && q.tile != 0) to = q.tile * w.tile;
+    }
+    __syncthreads();
+    rows[threadIdx.x] = to;
+    if (threadIdx.x == 0) rows[kScanThreads] = -1;
+    __syncthreads();
+    int k = 0;
+    for (bool more = true; more;) {
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        t[j] = live && k + j < kScanThreads && rows[k + j] >= 0 ? side.totals[(size_t)(c + step * (k + j)) * s.states + e] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int here = more ? rows[k] : -1;
+        if (here < 0) {
+          more = false;
+        } else {
+          // a share may be empty, and has no total then
+          if (here != from) x = fmaf(x, exp2f(g * (float)abs(here - from)), t[j]);
+          from = here;
+          ++k;
+          if (live) side.incoming[(size_t)(c + step * k) * s.states + e] = x;
+        }
+      }
+    }
+    if (k < kScanThreads) return;
+    c += step * kScanThreads;
   }
 }
 
