@@ -535,25 +535,29 @@ slim_status slim_decay_step_f32(const float *q, const float *k, const float *v, 
  *   over each group of each row,
  *   y = n * gamma + beta, times silu(gate) = gate / (1 + e^-gate) where gate is
  *   not NULL.
- * x, gate, y: dense bf16, or fp32 with _f32; gamma, beta: fp32 [cols].  y may
- * be neither x nor gate.  1 <= cols <= 16384, rows <= 2^30, else
+ * x, y: dense bf16, or fp32 with _f32; gate: the same type, rows gate_row
+ * elements apart (a part of a projection's rows); gamma, beta: fp32 [cols].  y
+ * may be neither x nor gate.  1 <= cols <= 16384, rows <= 2^30, else
  * SLIM_ERR_INVALID_ARG or SLIM_ERR_UNSUPPORTED; cols a multiple of groups;
  * eps >= 0.  Arithmetic is fp32, every result is rounded once. */
-slim_status slim_group_norm(const void *x, const float *gamma, const float *beta, const void *gate, float eps, void *y,
-                            int rows, int cols, int groups, slim_stream_t stream);
-slim_status slim_group_norm_f32(const float *x, const float *gamma, const float *beta, const float *gate, float eps,
-                                float *y, int rows, int cols, int groups, slim_stream_t stream);
+slim_status slim_group_norm(const void *x, const float *gamma, const float *beta, const void *gate,
+                            long long gate_row, float eps, void *y, int rows, int cols, int groups, slim_stream_t stream);
+slim_status slim_group_norm_f32(const float *x, const float *gamma, const float *beta, const float *gate,
+                                long long gate_row, float eps, float *y, int rows, int cols, int groups, slim_stream_t stream);
 
-/* Its gradients.  dgate: where the gate's goes (NULL without a gate).  dgamma,
+/* Its gradients.  dgate: where the gate's goes, rows dgate_row elements apart
+ * (NULL without a gate).  dgamma,
  * dbeta: fp32 [cols], overwritten, summed in an order that depends on the
  * shape alone; either may be NULL.  mean and rstd are formed again from x.
  * Outputs may not be inputs.  workspace: 16-byte aligned device memory of
  * slim_group_norm_bwd_workspace_bytes (needed for dgamma or dbeta only). */
 slim_status slim_group_norm_bwd(const void *dy, const void *x, const float *gamma, const float *beta, const void *gate,
-                                float eps, void *dx, void *dgate, float *dgamma, float *dbeta, void *workspace,
+                                long long gate_row, float eps, void *dx, void *dgate, long long dgate_row,
+                                float *dgamma, float *dbeta, void *workspace,
                                 size_t workspace_bytes, int rows, int cols, int groups, slim_stream_t stream);
 slim_status slim_group_norm_bwd_f32(const float *dy, const float *x, const float *gamma, const float *beta,
-                                    const float *gate, float eps, float *dx, float *dgate, float *dgamma, float *dbeta,
+                                    const float *gate, long long gate_row, float eps, float *dx, float *dgate,
+                                    long long dgate_row, float *dgamma, float *dbeta,
                                     void *workspace, size_t workspace_bytes, int rows, int cols, int groups,
                                     slim_stream_t stream);
 size_t slim_group_norm_bwd_workspace_bytes(int rows, int cols, int groups);

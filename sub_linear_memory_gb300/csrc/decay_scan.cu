@@ -85,13 +85,22 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(Prepare p) {
 
 constexpr int kScanThreads = 128;
 
+template <int VEC> struct Elements { using Type = float; };
+template <> struct Elements<4> { using Type = float4; };
+__device__ __forceinline__ float join(float x, float keep, float t) { return fmaf(x, keep, t); }
+__device__ __forceinline__ float4 join(float4 x, float keep, float4 t) {
+  return make_float4(fmaf(x.x, keep, t.x), fmaf(x.y, keep, t.y), fmaf(x.z, keep, t.z), fmaf(x.w, keep, t.w));
+}
+
 // Share c's incoming state from those of the shares before it (behind it in
 // reverse) in the same sequence.  A block goes along one sequence's shares
-// from the one that holds its beginning, for its own elements of the state.
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
+// from the one that holds its beginning, for its own elements of the state,
+// VEC to a thread.
+template <int VEC> __global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
   const Work &w = s.work;
   const auto &side = s.side[blockIdx.z];
-  const int e = blockIdx.x * kScanThreads + threadIdx.x;
+  using V = typename Elements<VEC>::Type;
+  const int e = (blockIdx.x * kScanThreads + threadIdx.x) * VEC;
   const int step = side.rev ? -1 : 1;
   int c = blockIdx.y;
   const Place begin = share_begin(w, c), end = share_begin(w, c + 1);
@@ -106,8 +115,9 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
   const float g = log2_decay(s.log_decay, edge.head);
   const bool live = e < s.states;
   long long at = side.start ? (side.place ? side.place[edge.seq] : edge.seq) : -1;
-  float x = at >= 0 && live ? side.start[((size_t)at * w.heads + edge.head) * s.states + e] : 0.f;
-  if (live && side.first) side.first[(size_t)c * s.states + e] = x;
+  V x{};
+  if (at >= 0 && live) x = *reinterpret_cast<const V *>(side.start + ((size_t)at * w.heads + edge.head) * s.states + e);
+  if (live && side.first) *reinterpret_cast<V *>(side.first + (size_t)c * s.states + e) = x;
   int from = side.rev ? b.y : 0;  // rows already passed lie before (behind) this one
   // The sequence's next shares, a block's threads' worth at a time: where each ends, from all threads at once; then
   // along them with eight totals on their way.
@@ -125,10 +135,12 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
     __syncthreads();
     int k = 0;
     for (bool more = true; more;) {
-      float t[8];
+      V t[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        t[j] = live && k + j < kScanThreads && rows[k + j] >= 0 ? side.totals[(size_t)(c + step * (k + j)) * s.states + e] : 0.f;
+        t[j] = live && k + j < kScanThreads && rows[k + j] >= 0
+                   ? *reinterpret_cast<const V *>(side.totals + (size_t)(c + step * (k + j)) * s.states + e)
+                   : V{};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int here = more ? rows[k] : -1;
@@ -136,10 +148,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
           more = false;
         } else {
           // a share may be empty, and has no total then
-          if (here != from) x = fmaf(x, exp2f(g * (float)abs(here - from)), t[j]);
+          if (here != from) x = join(x, exp2f(g * (float)abs(here - from)), t[j]);
           from = here;
           ++k;
-          if (live) side.incoming[(size_t)(c + step * k) * s.states + e] = x;
+          if (live) *reinterpret_cast<V *>(side.incoming + (size_t)(c + step * k) * s.states + e) = x;
         }
       }
     }
@@ -158,8 +170,14 @@ cudaError_t prepare(const Prepare &p, cudaStream_t st) {
 
 cudaError_t scan(const Scan &s, cudaStream_t st) {
   ProfScope ps("decay_scan", st);
-  const dim3 grid((s.states + kScanThreads - 1) / kScanThreads, s.work.parts, s.sides);
-  scan_kernel<<<grid, kScanThreads, 0, st>>>(s);
+  bool vec = s.states % 4 == 0;  // the workspace's parts are aligned, the caller's states may not be
+  for (int i = 0; i < s.sides; ++i) vec = vec && (reinterpret_cast<uintptr_t>(s.side[i].start) & 15) == 0;
+  const int each = kScanThreads * (vec ? 4 : 1);
+  const dim3 grid((s.states + each - 1) / each, s.work.parts, s.sides);
+  if (vec)
+    scan_kernel<4><<<grid, kScanThreads, 0, st>>>(s);
+  else
+    scan_kernel<1><<<grid, kScanThreads, 0, st>>>(s);
   return cudaGetLastError();
 }
 

@@ -56,6 +56,7 @@ __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f +
 struct Shape {
   int rows, cols, groups, width;
   float eps, inverse;  // 1 / width
+  long long gate_row, dgate_row;  // elements from row to row of the gate and its gradient
 };
 
 // The columns of a lane: its group, and piece i at column group * width + (lane % LANES + i LANES) VEC.
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       px[i].load(x + at + l.at(i), r < s.rows && l.has(s, i));
-      if (gate) pz[i].load(gate + at + l.at(i), r < s.rows && l.has(s, i));
+      if (gate) pz[i].load(gate + (long long)r * s.gate_row + l.first + l.at(i), r < s.rows && l.has(s, i));
     }
   };
   load(row);
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       const bool live = r < s.rows && l.has(s, i);
       px[i].load(x + at + l.at(i), live);
       pd[i].load(dy + at + l.at(i), live);
-      if (gate) pz[i].load(gate + at + l.at(i), live);
+      if (gate) pz[i].load(gate + (long long)r * s.gate_row + l.first + l.at(i), live);
     }
   };
   load(row);
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         h0 += d[i][j];
         h1 = fmaf(d[i][j], n, h1);
       }
-      if (gate) put<T, VEC>(dgate + at + l.at(i), l.has(s, i), z[i]);
+      if (gate) put<T, VEC>(dgate + (long long)row * s.dgate_row + l.first + l.at(i), l.has(s, i), z[i]);
     }
     h0 = group_sum<LANES>(h0) * s.inverse;
     h1 = group_sum<LANES>(h1) * s.inverse;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                         const T *__restrict__ gate, T *__restrict__ y, Shape s) {
   const int lane = threadIdx.x & 31, first = blockIdx.x * s.width;
   for (int row = blockIdx.y * kWarps + (threadIdx.x >> 5); row < s.rows; row += gridDim.y * kWarps) {
-    const long long at = (long long)row * s.cols + first;
+    const long long at = (long long)row * s.cols + first, gat = (long long)row * s.gate_row + first;
     float sum = 0.f, sq = 0.f;
     for (int c = lane; c < s.width; c += 32) sum += to_f32(x[at + c]);
     const float mean = group_sum<32>(sum) * s.inverse;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int c = lane; c < s.width; c += 32) {
       float v = fmaf((to_f32(x[at + c]) - mean) * rstd, gamma[first + c], beta[first + c]);
       if (gate) {
-        const float z = to_f32(gate[at + c]);
+        const float z = to_f32(gate[gat + c]);
         v *= z * sigmoid(z);
       }
       y[at + c] = from_f32<T>(v);
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   float *own = parts ? parts + (size_t)blockIdx.y * 2 * s.cols + first : nullptr;
   for (int b = 0; b < batches; ++b) {
     const int row0 = (b * gridDim.y + blockIdx.y) * kWarps, row = row0 + warp;
-    const long long at = (long long)row * s.cols + first;
+    const long long at = (long long)row * s.cols + first, gat = (long long)row * s.gate_row + first;
     if (row < s.rows) {
       float sum = 0.f, sq = 0.f, h0 = 0.f, h1 = 0.f;
       for (int c = lane; c < s.width; c += 32) sum += to_f32(x[at + c]);
@@ -282,8 +283,8 @@ __global__ void __launch_bounds__(kWarps * 32)
         const float n = (to_f32(x[at + c]) - mean) * rstd;
         float d = to_f32(dy[at + c]);
         if (gate) {
-          const float z = to_f32(gate[at + c]), sg = sigmoid(z);
-          dgate[at + c] = from_f32<T>(d * fmaf(n, gamma[first + c], beta[first + c]) * sg * fmaf(z, 1.f - sg, 1.f));
+          const float z = to_f32(gate[gat + c]), sg = sigmoid(z);
+          dgate[(long long)row * s.dgate_row + first + c] = from_f32<T>(d * fmaf(n, gamma[first + c], beta[first + c]) * sg * fmaf(z, 1.f - sg, 1.f));
           d *= z * sg;
         }
         d *= gamma[first + c];
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         const float n = (to_f32(x[at + c]) - mean) * rstd;
         float d = to_f32(dy[at + c]) * gamma[first + c];
         if (gate) {
-          const float z = to_f32(gate[at + c]);
+          const float z = to_f32(gate[gat + c]);
           d *= z * sigmoid(z);
         }
         dx[at + c] = from_f32<T>(rstd * (d - fmaf(n, h1, h0)));
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         const long long i = (long long)(row0 + k) * s.cols + first + c;
         float d = to_f32(dy[i]);
         if (gate) {
-          const float z = to_f32(gate[i]);
+          const float z = to_f32(gate[(long long)(row0 + k) * s.gate_row + first + c]);
           d *= z * sigmoid(z);
         }
         a = fmaf(d, (to_f32(x[i]) - stats[2 * k]) * stats[2 * k + 1], a);
@@ -381,18 +382,18 @@ Cut cut_for(int cols, int groups, bool vec) {
   M(8, 1, 1) M(8, 2, 1) M(8, 4, 1) M(8, 8, 1) M(8, 16, 1) M(8, 32, 1) M(8, 32, 2) M(8, 32, 4) M(1, 8, 1)  \
   M(1, 16, 1) M(1, 32, 1) M(1, 32, 4) M(1, 32, 16)
 
-Shape shape_of(int rows, int cols, int groups, float eps) {
-  return Shape{rows, cols, groups, cols / groups, eps, 1.f / (float)(cols / groups)};
+Shape shape_of(int rows, int cols, int groups, float eps, long long gate_row, long long dgate_row) {
+  return Shape{rows, cols, groups, cols / groups, eps, 1.f / (float)(cols / groups), gate_row, dgate_row};
 }
 
 }  // namespace
 
 template <typename T>
-cudaError_t group_norm(const void *x, const float *gamma, const float *beta, const void *gate, float eps, void *y,
-                       int rows, int cols, int groups, cudaStream_t st) {
+cudaError_t group_norm(const void *x, const float *gamma, const float *beta, const void *gate, long long gate_row,
+                       float eps, void *y, int rows, int cols, int groups, cudaStream_t st) {
   ProfScope ps("group_norm", st);
-  const Shape s = shape_of(rows, cols, groups, eps);
-  const Cut c = cut_for(cols, groups, q8::vector_rows(cols, {x, gate, y}));
+  const Shape s = shape_of(rows, cols, groups, eps, gate_row, 0);
+  const Cut c = cut_for(cols, groups, gate_row % 8 == 0 && q8::vector_rows(cols, {x, gate, y}));
   const dim3 grid(c.slabs(groups), row_blocks(rows, c.slabs(groups)));
   const T *xp = static_cast<const T *>(x), *zp = static_cast<const T *>(gate);
   T *yp = static_cast<T *>(y);
@@ -419,11 +420,12 @@ size_t group_norm_bwd_workspace(int rows, int cols, int groups) {
 
 template <typename T>
 cudaError_t group_norm_bwd(const void *dy, const void *x, const float *gamma, const float *beta, const void *gate,
-                           float eps, void *dx, void *dgate, float *dgamma, float *dbeta, void *workspace, int rows,
+                           long long gate_row, float eps, void *dx, void *dgate, long long dgate_row, float *dgamma, float *dbeta, void *workspace, int rows,
                            int cols, int groups, cudaStream_t st) {
   ProfScope ps("group_norm_bwd", st);
-  const Shape s = shape_of(rows, cols, groups, eps);
-  const Cut c = cut_for(cols, groups, q8::vector_rows(cols, {dy, x, gate, dx, dgate}));
+  const Shape s = shape_of(rows, cols, groups, eps, gate_row, dgate_row);
+  const Cut c = cut_for(cols, groups,
+                        gate_row % 8 == 0 && dgate_row % 8 == 0 && q8::vector_rows(cols, {dy, x, gate, dx, dgate}));
   const dim3 grid(c.slabs(groups), row_blocks(rows, c.slabs(groups)));
   const T *dp = static_cast<const T *>(dy), *xp = static_cast<const T *>(x), *zp = static_cast<const T *>(gate);
   T *dxp = static_cast<T *>(dx), *dzp = static_cast<T *>(dgate);
@@ -448,10 +450,11 @@ cudaError_t group_norm_bwd(const void *dy, const void *x, const float *gamma, co
 }
 
 #define SLIM_GN_FOR(T)                                                                                             \
-  template cudaError_t group_norm<T>(const void *, const float *, const float *, const void *, float, void *, int, \
-                                     int, int, cudaStream_t);                                                      \
+  template cudaError_t group_norm<T>(const void *, const float *, const float *, const void *, long long, float,   \
+                                     void *, int, int, int, cudaStream_t);                                         \
   template cudaError_t group_norm_bwd<T>(const void *, const void *, const float *, const float *, const void *,   \
-                                         float, void *, void *, float *, float *, void *, int, int, int,           \
+                                         long long, float, void *, void *, long long, float *, float *, void *,    \
+                                         int, int, int,                                                            \
                                          cudaStream_t);
 SLIM_GN_FOR(float)
 SLIM_GN_FOR(__nv_bfloat16)

@@ -9,14 +9,14 @@
 
 namespace slim {
 
-// group_norm.cu.  gate: NULL, or z.
+// group_norm.cu.  gate: NULL, or z, rows gate_row elements apart.
 template <typename T>
-cudaError_t group_norm(const void *x, const float *gamma, const float *beta, const void *gate, float eps, void *y,
-                       int rows, int cols, int groups, cudaStream_t st);
+cudaError_t group_norm(const void *x, const float *gamma, const float *beta, const void *gate, long long gate_row,
+                       float eps, void *y, int rows, int cols, int groups, cudaStream_t st);
 size_t group_norm_bwd_workspace(int rows, int cols, int groups);
 template <typename T>
 cudaError_t group_norm_bwd(const void *dy, const void *x, const float *gamma, const float *beta, const void *gate,
-                           float eps, void *dx, void *dgate, float *dgamma, float *dbeta, void *workspace, int rows,
+                           long long gate_row, float eps, void *dx, void *dgate, long long dgate_row, float *dgamma, float *dbeta, void *workspace, int rows,
                            int cols, int groups, cudaStream_t st);
 
 // adamw.cu

@@ -47,8 +47,8 @@ slim_status check_ptr(const void *p, size_t size) {
 }
 
 template <typename T>
-slim_status run_norm(const void *x, const float *gamma, const float *beta, const void *gate, float eps, void *y,
-                     int rows, int cols, int groups, cudaStream_t st) {
+slim_status run_norm(const void *x, const float *gamma, const float *beta, const void *gate, long long gate_row,
+                     float eps, void *y, int rows, int cols, int groups, cudaStream_t st) {
   NvtxRange range("slim_group_norm");
   SLIM_TRY(check_sizes(rows, cols, groups, eps));
   if (rows == 0) return SLIM_OK;
@@ -57,14 +57,15 @@ slim_status run_norm(const void *x, const float *gamma, const float *beta, const
   SLIM_TRY(check_ptr(beta, 4));
   SLIM_TRY(check_ptr(y, sizeof(T)));
   if (y == x || y == gate) return SLIM_ERR_INVALID_ARG;
+  if (gate && rows > 1 && gate_row < cols) return SLIM_ERR_INVALID_ARG;
   if (!aligned(gate, sizeof(T))) return SLIM_ERR_UNSUPPORTED;
-  return finish(group_norm<T>(x, gamma, beta, gate, eps, y, rows, cols, groups, st), st);
+  return finish(group_norm<T>(x, gamma, beta, gate, gate ? gate_row : 0, eps, y, rows, cols, groups, st), st);
 }
 
 template <typename T>
 slim_status run_norm_bwd(const void *dy, const void *x, const float *gamma, const float *beta, const void *gate,
-                         float eps, void *dx, void *dgate, float *dgamma, float *dbeta, void *workspace,
-                         size_t workspace_bytes, int rows, int cols, int groups, cudaStream_t st) {
+                         long long gate_row, float eps, void *dx, void *dgate, long long dgate_row, float *dgamma,
+                         float *dbeta, void *workspace, size_t workspace_bytes, int rows, int cols, int groups, cudaStream_t st) {
   NvtxRange range("slim_group_norm_bwd");
   SLIM_TRY(check_sizes(rows, cols, groups, eps));
   if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return SLIM_ERR_UNSUPPORTED;
@@ -78,7 +79,7 @@ slim_status run_norm_bwd(const void *dy, const void *x, const float *gamma, cons
   SLIM_TRY(check_ptr(gamma, 4));
   SLIM_TRY(check_ptr(beta, 4));
   SLIM_TRY(check_ptr(dx, sizeof(T)));
-  if (!gate != !dgate) return SLIM_ERR_INVALID_ARG;
+  if (!gate != !dgate || (gate && rows > 1 && (gate_row < cols || dgate_row < cols))) return SLIM_ERR_INVALID_ARG;
   if (!aligned(gate, sizeof(T)) || !aligned(dgate, sizeof(T))) return SLIM_ERR_UNSUPPORTED;
   for (const void *out : {dx, dgate})
     if (out && (out == dy || out == x || out == gate)) return SLIM_ERR_INVALID_ARG;
@@ -87,7 +88,7 @@ slim_status run_norm_bwd(const void *dy, const void *x, const float *gamma, cons
     if (!workspace || workspace_bytes < group_norm_bwd_workspace(rows, cols, groups)) return SLIM_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return SLIM_ERR_UNSUPPORTED;
   }
-  return finish(group_norm_bwd<T>(dy, x, gamma, beta, gate, eps, dx, dgate, dgamma, dbeta, workspace, rows, cols,
+  return finish(group_norm_bwd<T>(dy, x, gamma, beta, gate, gate ? gate_row : 0, eps, dx, dgate, gate ? dgate_row : 0, dgamma, dbeta, workspace, rows, cols,
                                   groups, st),
                 st);
 }
@@ -122,28 +123,29 @@ using namespace slim;
 
 extern "C" {
 
-slim_status slim_group_norm(const void *x, const float *gamma, const float *beta, const void *gate, float eps, void *y,
+slim_status slim_group_norm(const void *x, const float *gamma, const float *beta, const void *gate, long long gate_row, float eps, void *y,
                             int rows, int cols, int groups, slim_stream_t stream) {
-  return run_norm<bf16>(x, gamma, beta, gate, eps, y, rows, cols, groups, (cudaStream_t)stream);
+  return run_norm<bf16>(x, gamma, beta, gate, gate_row, eps, y, rows, cols, groups, (cudaStream_t)stream);
 }
 
-slim_status slim_group_norm_f32(const float *x, const float *gamma, const float *beta, const float *gate, float eps,
+slim_status slim_group_norm_f32(const float *x, const float *gamma, const float *beta, const float *gate, long long gate_row, float eps,
                                 float *y, int rows, int cols, int groups, slim_stream_t stream) {
-  return run_norm<float>(x, gamma, beta, gate, eps, y, rows, cols, groups, (cudaStream_t)stream);
+  return run_norm<float>(x, gamma, beta, gate, gate_row, eps, y, rows, cols, groups, (cudaStream_t)stream);
 }
 
 slim_status slim_group_norm_bwd(const void *dy, const void *x, const float *gamma, const float *beta, const void *gate,
-                                float eps, void *dx, void *dgate, float *dgamma, float *dbeta, void *workspace,
+                                long long gate_row, float eps, void *dx, void *dgate, long long dgate_row, float *dgamma, float *dbeta, void *workspace,
                                 size_t workspace_bytes, int rows, int cols, int groups, slim_stream_t stream) {
-  return run_norm_bwd<bf16>(dy, x, gamma, beta, gate, eps, dx, dgate, dgamma, dbeta, workspace, workspace_bytes, rows,
+  return run_norm_bwd<bf16>(dy, x, gamma, beta, gate, gate_row, eps, dx, dgate, dgate_row, dgamma, dbeta, workspace, workspace_bytes, rows,
                             cols, groups, (cudaStream_t)stream);
 }
 
 slim_status slim_group_norm_bwd_f32(const float *dy, const float *x, const float *gamma, const float *beta,
-                                    const float *gate, float eps, float *dx, float *dgate, float *dgamma, float *dbeta,
+                                    const float *gate, long long gate_row, float eps, float *dx, float *dgate,
+                                    long long dgate_row, float *dgamma, float *dbeta,
                                     void *workspace, size_t workspace_bytes, int rows, int cols, int groups,
                                     slim_stream_t stream) {
-  return run_norm_bwd<float>(dy, x, gamma, beta, gate, eps, dx, dgate, dgamma, dbeta, workspace, workspace_bytes, rows,
+  return run_norm_bwd<float>(dy, x, gamma, beta, gate, gate_row, eps, dx, dgate, dgate_row, dgamma, dbeta, workspace, workspace_bytes, rows,
                              cols, groups, (cudaStream_t)stream);
 }
 

@@ -173,7 +173,7 @@ def test_nothing_to_do(lib):
 def test_group_norm_refuses(lib, want, rows, cols, groups, eps, x, gate, y):
     from sub_linear_memory_gb300 import norm  # noqa: F401  (argument types)
 
-    assert lib.slim_group_norm(x, P[1], P[2], gate, eps, y, rows, cols, groups, None) == want
+    assert lib.slim_group_norm(x, P[1], P[2], gate, cols, eps, y, rows, cols, groups, None) == want
 
 
 @pytest.mark.parametrize("want, dx, dgate, gate, ws, n", [
@@ -183,7 +183,7 @@ def test_group_norm_refuses(lib, want, rows, cols, groups, eps, x, gate, y):
 def test_group_norm_bwd_refuses(lib, want, dx, dgate, gate, ws, n):
     from sub_linear_memory_gb300 import norm  # noqa: F401
 
-    assert lib.slim_group_norm_bwd(P[0], P[1], P[2], P[3], gate, 0.0, dx, dgate, P[7], P[8], ws, n, 4, 8, 2, None) == want
+    assert lib.slim_group_norm_bwd(P[0], P[1], P[2], P[3], gate, 8, 0.0, dx, dgate, 8, P[7], P[8], ws, n, 4, 8, 2, None) == want
 
 
 @pytest.mark.parametrize("want, change, entry", [
@@ -210,3 +210,12 @@ def test_adamw_needs_a_count_and_options(lib):
     assert lib.slim_adamw_f32(None, 0, ctypes.byref(o), None, None) == 1
     assert lib.slim_adamw_f32(None, 0, None, P[0], None) == 1
     assert lib.slim_adamw_f32(None, 2, ctypes.byref(o), P[0], None) == 1
+
+
+def test_group_norm_refuses_gates_whose_rows_overlap(lib):
+    from sub_linear_memory_gb300 import norm  # noqa: F401
+
+    assert lib.slim_group_norm(P[0], P[1], P[2], P[3], 7, 0.0, P[4], 4, 8, 2, None) == 1
+    for rows in ((7, 8), (8, 7)):
+        assert lib.slim_group_norm_bwd(P[0], P[1], P[2], P[3], P[4], rows[0], 0.0, P[5], P[6], rows[1], P[7], P[8], P[9], BIG, 4, 8, 2,
+                                       None) == 1

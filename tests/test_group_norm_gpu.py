@@ -109,6 +109,23 @@ def test_misaligned_rows(norm):
         assert np.linalg.norm(np64(s) - np64(t)) <= 4e-3 * np.linalg.norm(np64(t))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols, groups, pitch", [(512, 8, 1536), (96, 2, 200), (100, 4, 303), (2048, 1, 2056)])
+def test_gates_whose_rows_lie_apart(norm, cols, groups, pitch, dtype):
+    dy, x, gamma, beta, z = make(33, cols, dtype)
+    rows = draw((33, pitch), 9, dtype)
+    rows[:, 8:8 + cols] = z
+    out = rows.clone()
+    apart = rows[:, 8:8 + cols]
+    y, same = norm.group_norm(x, gamma, beta, groups, apart), norm.group_norm(x, gamma, beta, groups, z)
+    assert np.linalg.norm(np64(y) - np64(same)) <= (4e-3 if dtype == BF16 else 1e-6) * np.linalg.norm(np64(same))
+    want = norm.group_norm_bwd(dy, x, gamma, beta, groups, z)
+    got = norm.group_norm_bwd(dy, x, gamma, beta, groups, apart, dgate=out[:, 8:8 + cols])
+    for a, b in zip(got, want):  # an odd pitch takes another kernel, whose sums run in another order
+        assert np.linalg.norm(np64(a) - np64(b)) <= (4e-3 if dtype == BF16 else 1e-6) * np.linalg.norm(np64(b))
+    assert torch.equal(out[:, :8], rows[:, :8]) and torch.equal(out[:, 8 + cols:], rows[:, 8 + cols:])
+
+
 def test_equal_columns_and_eps(norm):
     """A group of equal values has no variance: n = 0, and with eps = 0 the result is NaN, as 0 times infinity is."""
     x = torch.full((2, 64), 3.0, dtype=BF16, device="cuda")
