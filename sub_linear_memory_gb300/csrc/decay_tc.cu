@@ -514,68 +514,68 @@ template <int D> __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tc_kerne
           const uint32_t b = slots + now.b * C::kSlot, c = slots + now.c * C::kSlot;
           const bool writes = !total && (!sums || g == groups - 1), update = sums || g == groups - 1;
           if (weighs) {
-          if (C::kStage == 0) {  // the ring is short: this unit's b may wait for it
-            if (lane == 0) give_back();
-            __syncwarp();
-          }
-          wait(full + units % kUnits, (units / kUnits) & 1);
-          if (!total) wait(scored + units % C::kBuffers, (units / C::kBuffers) & 1);  // the scores have read b
-          if (update) {
-            const uint32_t rest = weighted + (updates % C::kBuffers) * C::kRest, high = b;
-            if (updates >= C::kBuffers) wait(added + updates % C::kBuffers, (updates / C::kBuffers + 1) & 1);
-            ++updates;
-            // a row's sixteen-byte pieces lie at their place in the row's 128 bytes, exclusive-or the row's place in eight
-            const uint32_t at_row = (uint32_t)(t >> 3) * 1024u + (uint32_t)(t & 7) * 128u, swap = (uint32_t)(t & 7) << 4;
-            if (t < n) {
-              // two pieces of eight columns at a time, their loads ahead of the arithmetic
+            if (C::kStage == 0) {  // the ring is short: this unit's b may wait for it
+              if (lane == 0) give_back();
+              __syncwarp();
+            }
+            wait(full + units % kUnits, (units / kUnits) & 1);
+            if (!total) wait(scored + units % C::kBuffers, (units / C::kBuffers) & 1);  // the scores have read b
+            if (update) {
+              const uint32_t rest = weighted + (updates % C::kBuffers) * C::kRest, high = b;
+              if (updates >= C::kBuffers) wait(added + updates % C::kBuffers, (updates / C::kBuffers + 1) & 1);
+              ++updates;
+              // a row's sixteen-byte pieces lie at their place in the row's 128 bytes, exclusive-or the row's place in eight
+              const uint32_t at_row = (uint32_t)(t >> 3) * 1024u + (uint32_t)(t & 7) * 128u, swap = (uint32_t)(t & 7) << 4;
+              if (t < n) {
+                // two pieces of eight columns at a time, their loads ahead of the arithmetic
 #pragma unroll 1
-              for (int x = 0; x < D / 8; x += 2) {
-                const uint32_t half = at_row + (uint32_t)(x >> 3) * (kTile * 128u);
-                uint32_t off[2], raw[8], h[8], l[8];
+                for (int x = 0; x < D / 8; x += 2) {
+                  const uint32_t half = at_row + (uint32_t)(x >> 3) * (kTile * 128u);
+                  uint32_t off[2], raw[8], h[8], l[8];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  off[i] = half + ((uint32_t)(((x & 7) + i) << 4) ^ swap);
-                  ld_shared_v4(b + off[i], raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
-                }
+                  for (int i = 0; i < 2; ++i) {
+                    off[i] = half + ((uint32_t)(((x & 7) + i) << 4) ^ swap);
+                    ld_shared_v4(b + off[i], raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+                  }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(raw[j] << 16), __uint_as_float(raw[j] & 0xffff0000u)),
-                                              make_float2(weight, weight));
-                  h[j] = pack_bf16(v.x, v.y);
-                  // v - h, exactly
-                  const float2 r2 = __ffma2_rn(make_float2(__uint_as_float(h[j] << 16), __uint_as_float(h[j] & 0xffff0000u)),
-                                               make_float2(-1.f, -1.f), v);
-                  l[j] = pack_bf16(r2.x, r2.y);
-                }
+                  for (int j = 0; j < 8; ++j) {
+                    const float2 v = __fmul2_rn(make_float2(__uint_as_float(raw[j] << 16), __uint_as_float(raw[j] & 0xffff0000u)),
+                                                make_float2(weight, weight));
+                    h[j] = pack_bf16(v.x, v.y);
+                    // v - h, exactly
+                    const float2 r2 = __ffma2_rn(make_float2(__uint_as_float(h[j] << 16), __uint_as_float(h[j] & 0xffff0000u)),
+                                                 make_float2(-1.f, -1.f), v);
+                    l[j] = pack_bf16(r2.x, r2.y);
+                  }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  st_shared_v4(high + off[i], h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                  st_shared_v4(rest + off[i], l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+                  for (int i = 0; i < 2; ++i) {
+                    st_shared_v4(high + off[i], h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                    st_shared_v4(rest + off[i], l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+                  }
                 }
-              }
-            } else {
+              } else {
 #pragma unroll 1
-              for (int x = 0; x < D; x += 8) {
-                st_shared_v4(high + sw128_offset(t, x, kTile), 0, 0, 0, 0);
-                st_shared_v4(rest + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+                for (int x = 0; x < D; x += 8) {
+                  st_shared_v4(high + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+                  st_shared_v4(rest + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+                }
               }
             }
-          }
-          if (loads_bc(g) && t >= n) {
-            // rows behind the sequence: 0 times whatever they hold has to be 0
+            if (loads_bc(g) && t >= n) {
+              // rows behind the sequence: 0 times whatever they hold has to be 0
 #pragma unroll 1
-            for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
-          }
-          if (update || n < kTile) {
-            fence_async_smem();
-            named_barrier_sync(2, 128);
-          }
-          if (t == 0) mbar_arrive(turned + units % kUnits);
-          if (lane == 0) {
-            if (ends_bc(g)) mbar_arrive(empty + now.b);
-            if (!total && ends_a(g) && (C::kStage || !writes)) mbar_arrive(empty + now.a);
-            if (ends_bc(g)) mbar_arrive(empty + now.c);
-          }
+              for (int x = 0; x < D; x += 8) st_shared_v4(c + sw128_offset(t, x, kTile), 0, 0, 0, 0);
+            }
+            if (update || n < kTile) {
+              fence_async_smem();
+              named_barrier_sync(2, 128);
+            }
+            if (t == 0) mbar_arrive(turned + units % kUnits);
+            if (lane == 0) {
+              if (ends_bc(g)) mbar_arrive(empty + now.b);
+              if (!total && ends_a(g) && (C::kStage || !writes)) mbar_arrive(empty + now.a);
+              if (ends_bc(g)) mbar_arrive(empty + now.c);
+            }
           }
           if (!results) continue;
           // where the rows' warpgroup does both, the last unit's result, while the MMAs take what was handed out

@@ -19,10 +19,12 @@ them by the library, so no activation is kept in 16 bits.
 
 The computations are the library's; torch moves heads (rows [B L][heads d] to
 and from [B][heads][L][d]) and allocates.
+
+:class:`DecayLayer8` has the decay attention in the place of this one.
 """
 import torch
 
-from . import binding, q8
+from . import binding, decay, norm, q8
 
 
 class Layer8:
@@ -110,3 +112,83 @@ class Layer8:
         h2, y2, _, _ = q8.rms_norm(h, self.g2, res=p, eps=self.eps)
         a, _ = q8.gelu(q8.matmul(y2, self.w1), checkpoint=False)
         return h2, q8.matmul(a, self.w2)
+
+
+class DecayLayer8(Layer8):
+    """The same layer with an attention that forgets: a decay for each
+    key-value head, grouped query heads, packed sequences, and a group norm of
+    each head's output with a gate.  With (x, r) as before,
+
+        h  = x + r              y  = 8 bits of norm(h) g1
+        q, k, v, z = y Win^T    o  = decay attention(q, k, v)
+        u  = group norm(o) silu(z)
+        h2 = h + 8bits(u) Wo^T  and the feed-forward block.
+
+    Kept for the backward besides: o in 16 bits, whose norm is formed again.
+
+    heads, kv_heads: heads a multiple of kv_heads, heads * d = d_model.
+    log_decay: fp32 [kv_heads].  win [(2 heads + 2 kv_heads) d, d_model]: the
+    rows of q, k, v and z; wo, w1, w2, g1, g2 as in Layer8; gn, bn fp32
+    [d_model]: the group norm's weight and bias."""
+
+    NAMES = ("win", "wo", "w1", "w2")
+
+    def __init__(self, heads, kv_heads, log_decay, win, wo, w1, w2, g1, g2, gn, bn, eps=1e-5):
+        self.heads, self.kv_heads, self.log_decay, self.eps = heads, kv_heads, log_decay, eps
+        self.g1, self.g2, self.gn, self.bn = g1, g2, gn, bn
+        self.d = g1.shape[0] // heads
+        self.scale = self.d ** -0.5
+        self.load(win=win, wo=wo, w1=w1, w2=w2)
+
+    def _parts(self, rows):
+        """Rows of Win's product -> views of q, k, v [rows, heads, d] and z [rows, heads d]."""
+        n, h, k, d = rows.shape[0], self.heads, self.kv_heads, self.d
+        q, key, v, z = rows.split((h * d, k * d, k * d, h * d), dim=1)
+        return q.view(n, h, d), key.view(n, k, d), v.view(n, k, d), z
+
+    def _mix(self, rows, cu_seqlens, **states):
+        q, k, v, z = self._parts(rows)
+        o = decay.attn(q, k, v, self.log_decay, cu_seqlens, self.scale, **states).view(rows.shape[0], self.heads * self.d)
+        return o, norm.group_norm(o, self.gn, self.bn, self.heads, z, self.eps)
+
+    def forward(self, x, r, cu_seqlens):
+        """x, r: bf16 rows [T][d_model] of the sequences [cu_seqlens[i], cu_seqlens[i + 1])."""
+        h, y, rstd, h8 = q8.rms_norm(x, self.g1, res=r, eps=self.eps, checkpoint=True)
+        o, u = self._mix(q8.matmul(y, self.win), cu_seqlens)
+        u8 = q8.quantize(u)
+        h2, y2, rstd2, h28 = q8.rms_norm(h, self.g2, res=q8.matmul(u8, self.wo), eps=self.eps, checkpoint=True)
+        a, z8 = q8.gelu(q8.matmul(y2, self.w1))
+        return (h2, q8.matmul(a, self.w2)), (cu_seqlens, h8, y, rstd, o, u8, h28, y2, rstd2, z8, a)
+
+    def backward(self, dh2, df, kept):
+        """Gradients of forward's pair -> (gradient of x and of r, {name: gradient})."""
+        cu_seqlens, h8, y, rstd, o, u8, h28, y2, rstd2, z8, a = kept
+        grads = {"w2": q8.wgrad(df, a)}
+        dz, dz8 = q8.gelu_bwd(q8.matmul(q8.quantize(df), self.w2_t), z8, quantized=True)
+        grads["w1"] = q8.wgrad(dz, y2)
+        dh2, grads["g2"] = q8.rms_norm_bwd(q8.matmul(dz8, self.w1_t), h28, rstd2, self.g2, dres=dh2)
+        grads["wo"] = q8.wgrad(dh2, u8)
+        rows = q8.matmul(y, self.win)
+        q, k, v, z = self._parts(rows)
+        drows = torch.empty_like(rows)
+        dq, dk, dv, dgate = self._parts(drows)
+        du = q8.matmul(q8.quantize(dh2), self.wo_t)
+        do, _, grads["gn"], grads["bn"] = norm.group_norm_bwd(du, o, self.gn, self.bn, self.heads, z, self.eps, dgate=dgate)
+        decay.attn_bwd(q, k, v, self.log_decay, do.view(q.shape), cu_seqlens, self.scale, out=(dq, dk, dv))
+        grads["win"] = q8.wgrad(drows, y)
+        dh, grads["g1"] = q8.rms_norm_bwd(q8.matmul(q8.quantize(drows), self.win_t), h8, rstd, self.g1, dres=dh2)
+        return dh, grads
+
+    def prefill(self, x, r, cu_seqlens, state, slots=None):
+        """forward for serving, from the states (fp32 [places][kv_heads][d][d]) that the sequences have, which
+        are advanced in place; slots: the sequences' places."""
+        h, y, _, _ = q8.rms_norm(x, self.g1, res=r, eps=self.eps)
+        _, u = self._mix(q8.matmul(y, self.win), cu_seqlens, state_in=state, state_out=state, slots=slots)
+        return self._finish(h, u)
+
+    def decode(self, x, r, state, slots=None):
+        """One token for each of B sequences: x, r [B][d_model]; state is advanced in place."""
+        h, y, _, _ = q8.rms_norm(x, self.g1, res=r, eps=self.eps)
+        q, k, v, z = self._parts(q8.matmul(y, self.win))
+        o = decay.step(q, k, v, self.log_decay, state, slots, self.scale).view(x.shape[0], self.heads * self.d)
+        return self._finish(h, norm.group_norm(o, self.gn, self.bn, self.heads, z, self.eps))
