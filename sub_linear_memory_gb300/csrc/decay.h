@@ -23,10 +23,31 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "../../include/slim_attn.h"
 
 namespace slim {
 namespace decay {
+
+// A kernel's leave to use more than 48 KB of shared memory, asked for once on
+// each device (a call to the driver costs as much as a launch).
+class SharedMemory {
+ public:
+  template <typename K> cudaError_t allow(K kernel, size_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<size_t> &most = most_[dev & 63];
+    if (dev < 64 && most.load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) most.store(bytes, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  std::atomic<size_t> most_[64] = {};
+};
 
 // The list of tiles.
 struct Work {

@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kThreads) mix_kernel(Launch l) {
 
 template <typename T, int TILE> cudaError_t launch(const Launch &l, int widest_x, int widest_y, cudaStream_t st) {
   const size_t bytes = smem_bytes<TILE>(widest_x);
-  cudaError_t e = cudaFuncSetAttribute(mix_kernel<T, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  static SharedMemory allowed;
+  cudaError_t e = allowed.allow(mix_kernel<T, TILE>, smem_bytes<TILE>(TILE == 64 ? 128 : 256));
   if (e != cudaSuccess) return e;
   const dim3 grid(l.work.parts, (widest_y + kCols - 1) / kCols, l.mixes);
   mix_kernel<T, TILE><<<grid, kThreads, bytes, st>>>(l);

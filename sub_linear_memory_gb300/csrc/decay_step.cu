@@ -104,7 +104,8 @@ template <typename T> cudaError_t step(const Step &s, cudaStream_t st) {
   const size_t bytes = sizeof(float) * ((size_t)s.dk * (1 + s.groups) + (size_t)rows * s.groups * s.dv);
   auto kernel = vec ? step_kernel<T, 4> : step_kernel<T, 1>;
   if (bytes > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static SharedMemory allowed[2];
+    cudaError_t e = allowed[vec].allow(kernel, 200 * 1024);  // 64 query heads take 195 KB at most
     if (e != cudaSuccess) return e;
   }
   kernel<<<s.heads * s.rows, kThreads, bytes, st>>>(s);

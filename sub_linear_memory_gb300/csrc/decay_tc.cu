@@ -43,14 +43,14 @@ constexpr int kTile = 128;
 constexpr uint32_t kGiveUp = 1u << 21;  // tries of a wait, each of which may sleep for a while: a second or more
 constexpr int kUnits = 16;  // barriers of units in a row: more than the ring holds
 
-template <int D> struct Cfg {
+template <int D, bool TOTAL> struct Cfg {
   static constexpr uint32_t kSlot = kTile * D * 2;     // a tile of one operand
   // At D = 64 a warpgroup of its own writes the results; at 128 the state's registers leave none.  Registers of the
   // warpgroups (loads and MMAs, weighted scores, rows, results, state): at most 640 x 96 or 512 x 128 in all.
-  static constexpr bool kWriters = D == 64;
-  static constexpr int kThreads = D == 64 ? 640 : 512;
-  static constexpr int kRegs0 = D == 64 ? 88 : 96, kRegsScores = D == 64 ? 112 : 128, kRegsRows = D == 64 ? 72 : 80,
-                       kRegsState = D == 64 ? 120 : 208;
+  static constexpr bool kWriters = D == 64 && !TOTAL;
+  static constexpr int kThreads = kWriters ? 640 : 512;
+  static constexpr int kRegs0 = kWriters ? 88 : 96, kRegsScores = kWriters ? 112 : 128, kRegsRows = kWriters ? 72 : 80,
+                       kRegsState = kWriters ? 120 : 208;
   static constexpr int kSlots = D == 64 ? 9 : 5;
   static constexpr int kBuffers = D == 64 ? 2 : 1;     // of scores, b~, X and updates
   static constexpr uint32_t kRest = kSlot;             // b~: remainders; its high parts take b's place
@@ -86,8 +86,8 @@ __device__ __forceinline__ uint64_t with_lbo(uint64_t desc, uint32_t bytes) {
   return (desc & ~((uint64_t)0x3FFF << 16)) | (uint64_t)((bytes >> 4) & 0x3FFF) << 16;
 }
 
-template <int D> __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tc_kernel(const __grid_constant__ Args p) {
-  using C = Cfg<D>;
+template <int D, bool TOTAL> __global__ void __launch_bounds__(Cfg<D, TOTAL>::kThreads, 1) tc_kernel(const __grid_constant__ Args p) {
+  using C = Cfg<D, TOTAL>;
   extern __shared__ char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   char *generic = smem_raw + (base - smem_u32(smem_raw));
@@ -104,7 +104,8 @@ template <int D> __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tc_kerne
   const int part = blockIdx.x / p.mixes, which = blockIdx.x - part * p.mixes;
   const Mix &m = p.mix[which];
   const Work &w = p.work;
-  const bool total = m.totals != nullptr, sums = m.b_heads > 1;
+  constexpr bool total = TOTAL;  // the totals of the shares alone
+  const bool sums = m.b_heads > 1;
   const int groups = max(m.a_heads, m.b_heads);
 
   if (threadIdx.x == 0) {
@@ -691,10 +692,12 @@ template <int D> __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tc_kerne
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D> cudaError_t launch(const Args &a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kBytes);
+template <int D, bool TOTAL> cudaError_t launch(const Args &a, cudaStream_t st) {
+  using C = Cfg<D, TOTAL>;
+  static SharedMemory allowed;
+  cudaError_t e = allowed.allow(tc_kernel<D, TOTAL>, C::kBytes);
   if (e != cudaSuccess) return e;
-  tc_kernel<D><<<a.work.parts * a.mixes, Cfg<D>::kThreads, Cfg<D>::kBytes, st>>>(a);
+  tc_kernel<D, TOTAL><<<a.work.parts * a.mixes, C::kThreads, C::kBytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -752,7 +755,9 @@ cudaError_t mix_tc(const Launch &l, int *status, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   for (int i = used; i < 4; ++i) a.maps[i] = a.maps[0];
-  return l.mix[0].x == 64 ? launch<64>(a, st) : launch<128>(a, st);
+  const bool total = l.mix[0].totals != nullptr;
+  if (l.mix[0].x == 64) return total ? launch<64, true>(a, st) : launch<64, false>(a, st);
+  return total ? launch<128, true>(a, st) : launch<128, false>(a, st);
 }
 
 }  // namespace decay

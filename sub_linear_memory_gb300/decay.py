@@ -118,15 +118,38 @@ def _slots(slots, n, device):
         raise ValueError("slots must be a contiguous int32 [%d] tensor on q's device" % n)
 
 
-def _out(t, what, shape, like):
-    if t is None:
-        t = torch.empty(shape, dtype=like.dtype, device=like.device)
-    return t, _row(t, what, shape, like)
+# What calls of one layout share: the checked slim_decay_shape, the output's shape, and the workspace's bytes.
+# The checks and queries cost as much as a short call's kernels.
+_known = {}
 
 
-def _workspace(shape, cu_seqlens, bwd, device):
-    n = _lib.slim_decay_workspace_bytes(ctypes.byref(shape), cu_seqlens is None, bwd)
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+def _layout(*tensors):
+    return tuple(None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors)
+
+
+def _remember(key, plan):
+    if len(_known) >= 4096:
+        _known.clear()
+    _known[key] = plan
+    return plan
+
+
+def _bytes(shape, cu_seqlens, bwd):
+    return _lib.slim_decay_workspace_bytes(ctypes.byref(shape), cu_seqlens is None, bwd)
+
+
+def _plan_attn(q, k, v, log_decay, cu_seqlens, state_in, state_out, slots, seqs, out):
+    key = (0, seqs) + _layout(q, k, v, log_decay, cu_seqlens, state_in, state_out, slots, out)
+    plan = _known.get(key)
+    if plan is not None:
+        return plan
+    shape = _check(q, k, v, log_decay)
+    _seqs(shape, cu_seqlens, seqs, q.device)
+    _slots(slots, shape.seqs, q.device)
+    _states(shape, q.device, None if slots is not None else shape.seqs, state_in=state_in, state_out=state_out)
+    o = (q.shape[0], q.shape[1], shape.dv)
+    shape.o_row = q.shape[1] * shape.dv if out is None else _row(out, "out", o, q)
+    return _remember(key, (shape, o, _bytes(shape, cu_seqlens, 0)))
 
 
 def attn(q, k, v, log_decay, cu_seqlens=None, scale=1.0, state_in=None, state_out=None, slots=None, seqs=1, out=None):
@@ -137,37 +160,59 @@ def attn(q, k, v, log_decay, cu_seqlens=None, scale=1.0, state_in=None, state_ou
     sequence's place in the states (without it, sequence i has place i); one
     that names no place, or another's, starts from zero and leaves no state.
     Rows outside every sequence are not written."""
-    shape = _check(q, k, v, log_decay)
+    shape, o, nbytes = _plan_attn(q, k, v, log_decay, cu_seqlens, state_in, state_out, slots, seqs, out)
     device = q.device
-    _seqs(shape, cu_seqlens, seqs, device)
-    _slots(slots, shape.seqs, device)
-    _states(shape, device, None if slots is not None else shape.seqs, state_in=state_in, state_out=state_out)
-    out, shape.o_row = _out(out, "out", (q.shape[0], q.shape[1], shape.dv), q)
-    ws, n = _workspace(shape, cu_seqlens, 0, device)
+    if out is None:
+        out = torch.empty(o, dtype=q.dtype, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     _call("slim_decay_fwd", q.dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(cu_seqlens),
-          _ptr(state_in), _ptr(state_out), _ptr(slots), out.data_ptr(), ctypes.byref(shape), scale, ws.data_ptr(), n,
+          _ptr(state_in), _ptr(state_out), _ptr(slots), out.data_ptr(), ctypes.byref(shape), scale, ws.data_ptr(), nbytes,
           _stream(device))
     return out
+
+
+def _plan_bwd(q, k, v, log_decay, do, cu_seqlens, state_in, g_in, g_out, seqs, out):
+    key = (1, seqs) + _layout(q, k, v, log_decay, do, cu_seqlens, state_in, g_in, g_out, *(out or ()))
+    plan = _known.get(key)
+    if plan is not None:
+        return plan
+    shape = _check(q, k, v, log_decay)
+    _seqs(shape, cu_seqlens, seqs, q.device)
+    _states(shape, q.device, shape.seqs, state_in=state_in, g_in=g_in, g_out=g_out)
+    shape.o_row = _row(do, "do", (q.shape[0], q.shape[1], shape.dv), q)
+    dq, dk, dv = out if out is not None else (None, None, None)
+    dense = lambda t: t.shape[1] * t.shape[2]
+    shape.dq_row = dense(q) if dq is None else _row(dq, "dq", q.shape, q)
+    shape.dk_row = dense(k) if dk is None else _row(dk, "dk", k.shape, q)
+    shape.dv_row = dense(v) if dv is None else _row(dv, "dv", v.shape, q)
+    return _remember(key, (shape, _bytes(shape, cu_seqlens, 1)))
 
 
 def attn_bwd(q, k, v, log_decay, do, cu_seqlens=None, scale=1.0, state_in=None, g_in=None, g_out=None, seqs=1, out=None):
     """(dq, dk, dv) of :func:`attn`: do is the gradient of o, g_in (or None)
     that of the states behind the last rows; g_out (or None) receives that of
     state_in.  out: buffers for the three, whose rows may lie apart."""
-    shape = _check(q, k, v, log_decay)
+    shape, nbytes = _plan_bwd(q, k, v, log_decay, do, cu_seqlens, state_in, g_in, g_out, seqs, out)
     device = q.device
-    _seqs(shape, cu_seqlens, seqs, device)
-    _states(shape, device, shape.seqs, state_in=state_in, g_in=g_in, g_out=g_out)
-    shape.o_row = _row(do, "do", (q.shape[0], q.shape[1], shape.dv), q)
-    dq, dk, dv = out if out is not None else (None, None, None)
-    dq, shape.dq_row = _out(dq, "dq", q.shape, q)
-    dk, shape.dk_row = _out(dk, "dk", k.shape, q)
-    dv, shape.dv_row = _out(dv, "dv", v.shape, q)
-    ws, n = _workspace(shape, cu_seqlens, 1, device)
+    dq, dk, dv = out if out is not None else (torch.empty(t.shape, dtype=q.dtype, device=device) for t in (q, k, v))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     _call("slim_decay_bwd", q.dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(cu_seqlens),
           do.data_ptr(), _ptr(state_in), _ptr(g_in), _ptr(g_out), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-          ctypes.byref(shape), scale, ws.data_ptr(), n, _stream(device))
+          ctypes.byref(shape), scale, ws.data_ptr(), nbytes, _stream(device))
     return dq, dk, dv
+
+
+def _plan_step(q, k, v, log_decay, state, slots, out):
+    key = (2,) + _layout(q, k, v, log_decay, state, slots, out)
+    plan = _known.get(key)
+    if plan is not None:
+        return plan
+    shape = _check(q, k, v, log_decay)
+    _slots(slots, shape.tokens, q.device)
+    _states(shape, q.device, None if slots is not None else shape.tokens, state=state)
+    o = (q.shape[0], q.shape[1], shape.dv)
+    shape.o_row = q.shape[1] * shape.dv if out is None else _row(out, "out", o, q)
+    return _remember(key, (shape, o))
 
 
 def step(q, k, v, log_decay, state, slots=None, scale=1.0, out=None):
@@ -175,11 +220,10 @@ def step(q, k, v, log_decay, state, slots=None, scale=1.0, out=None):
     -> o [B, Hq, dv]; ``state`` is advanced in place.  slots: int32 [B], each
     row's place in it (without it, row i has place i); a row that names no
     place, or an earlier row's, gets zeros."""
-    shape = _check(q, k, v, log_decay)
+    shape, o = _plan_step(q, k, v, log_decay, state, slots, out)
     device = q.device
-    _slots(slots, shape.tokens, device)
-    _states(shape, device, None if slots is not None else shape.tokens, state=state)
-    out, shape.o_row = _out(out, "out", (q.shape[0], q.shape[1], shape.dv), q)
+    if out is None:
+        out = torch.empty(o, dtype=q.dtype, device=device)
     _call("slim_decay_step", q.dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
           _ptr(slots), out.data_ptr(), ctypes.byref(shape), scale, _stream(device))
     return out
