@@ -471,8 +471,9 @@ size_t slim_q8_wgrad_workspace_bytes(int rows, int n, int k);
  * sums are fp32.  In bf16 a weighted score (q . k) lambda^n is rounded to bf16
  * before its product with v where the tensor cores run, and so is the state
  * before its product with q (2^-9 of each term, as the result's own rounding).
- * A NaN or an infinity in a row also reaches earlier rows of its own sequence
- * within 128 rows before it (0 times it is NaN), and no other sequence.
+ * A NaN or an infinity in a row also reaches other rows of its own sequence
+ * within the 128 rows of a tile (0 times it is NaN), and no other sequence.
+ * The states' sums take bf16 rows with their weights as numbers of 17 bits.
  * Results depend on shape and lengths alone, not on timing.
  *
  * Tensors must not overlap, but for state_out = state_in.  workspace: device
