@@ -11,7 +11,7 @@ namespace decay {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMaxGroups = 8;  // query heads of one pass over the columns
+constexpr int kBatch = 8;
 
 // The row that has this slot: the first of those that name it.
 __device__ __forceinline__ bool taken_before(const int *slots, int row, int slot) {
@@ -21,8 +21,10 @@ __device__ __forceinline__ bool taken_before(const int *slots, int row, int slot
 }
 
 // A block has one key-value head of one row; VEC columns and every
-// (threads / (dv / VEC))-th row of the state are one thread's.
-template <typename T, int VEC>
+// (threads / (dv / VEC))-th row of the state are one thread's, kBatch rows at a
+// time with their loads ahead of the stores: a row at a time (each load behind
+// the last row's store) took 22 us for 128 rows of 16 heads of 64, this way TIME.
+template <typename T, int VEC, int MOST>
 __global__ void __launch_bounds__(kThreads) step_kernel(Step s) {
   extern __shared__ float sm[];
   const int head = blockIdx.x % s.heads, row = blockIdx.x / s.heads, t = threadIdx.x;
@@ -52,35 +54,45 @@ __global__ void __launch_bounds__(kThreads) step_kernel(Step s) {
     float v[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] = col * VEC + i < s.dv ? to_f32(vp[col * VEC + i]) : 0.f;
-    for (int g0 = 0; g0 < s.groups; g0 += kMaxGroups) {
-      float acc[kMaxGroups][VEC] = {};
-      for (int r = r0; r < s.dk; r += rows) {
-        float *p = state + (size_t)r * s.dv + col * VEC;
-        float x[VEC];
-        if constexpr (VEC == 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(p);
-          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-        } else {
-          x[0] = *p;
-        }
-        if (g0 == 0) {
+    for (int g0 = 0; g0 < s.groups; g0 += MOST) {
+      float acc[MOST][VEC] = {};
+      for (int rb = r0; rb < s.dk; rb += rows * kBatch) {
+        float x[kBatch][VEC];
+        float *p = state + (size_t)rb * s.dv + col * VEC;
+        const size_t next = (size_t)rows * s.dv;
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) x[i] = fmaf(x[i], lambda, k[r] * v[i]);
-          if constexpr (VEC == 4)
-            *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-          else
-            *p = x[0];
-        }
-#pragma unroll
-        for (int g = 0; g < kMaxGroups; ++g)
-          if (g0 + g < s.groups) {
-            const float qv = q[(g0 + g) * s.dk + r];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[g][i] = fmaf(qv, x[i], acc[g][i]);
+        for (int b = 0; b < kBatch; ++b) {
+          if (rb + b * rows >= s.dk) continue;
+          if constexpr (VEC == 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(p + b * next);
+            x[b][0] = f.x, x[b][1] = f.y, x[b][2] = f.z, x[b][3] = f.w;
+          } else {
+            x[b][0] = p[b * next];
           }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int r = rb + b * rows;
+          if (r >= s.dk) continue;
+          if (g0 == 0) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[b][i] = fmaf(x[b][i], lambda, k[r] * v[i]);
+            if constexpr (VEC == 4)
+              *reinterpret_cast<float4 *>(p + b * next) = make_float4(x[b][0], x[b][1], x[b][2], x[b][3]);
+            else
+              p[b * next] = x[b][0];
+          }
+#pragma unroll
+          for (int g = 0; g < MOST; ++g)
+            if (g0 + g < s.groups) {
+              const float qv = q[(g0 + g) * s.dk + r];
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) acc[g][i] = fmaf(qv, x[b][i], acc[g][i]);
+            }
+        }
       }
 #pragma unroll
-      for (int g = 0; g < kMaxGroups; ++g)
+      for (int g = 0; g < MOST; ++g)
         if (g0 + g < s.groups)
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
@@ -102,10 +114,12 @@ template <typename T> cudaError_t step(const Step &s, cudaStream_t st) {
   const bool vec = s.dv % 4 == 0 && (reinterpret_cast<uintptr_t>(s.state) & 15) == 0;
   const int cols = vec ? s.dv / 4 : s.dv, rows = kThreads / min(cols, kThreads);
   const size_t bytes = sizeof(float) * ((size_t)s.dk * (1 + s.groups) + (size_t)rows * s.groups * s.dv);
-  auto kernel = vec ? step_kernel<T, 4> : step_kernel<T, 1>;
+  // query heads of one pass over the state: one, or up to four
+  const bool one = s.groups == 1;
+  auto kernel = vec ? (one ? step_kernel<T, 4, 1> : step_kernel<T, 4, 4>) : (one ? step_kernel<T, 1, 1> : step_kernel<T, 1, 4>);
   if (bytes > 48 * 1024) {
-    static SharedMemory allowed[2];
-    cudaError_t e = allowed[vec].allow(kernel, 200 * 1024);  // 64 query heads take 195 KB at most
+    static SharedMemory allowed[4];
+    cudaError_t e = allowed[2 * vec + one].allow(kernel, 200 * 1024);  // 64 query heads take 193 KB at most
     if (e != cudaSuccess) return e;
   }
   kernel<<<s.heads * s.rows, kThreads, bytes, st>>>(s);

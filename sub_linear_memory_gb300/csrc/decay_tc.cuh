@@ -654,6 +654,12 @@ __global__ void __launch_bounds__(Cfg<D, TOTAL>::kThreads, 1) tc_kernel(const __
       } else if (m.transposed) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) s[i] = start[first + i * D];
+      } else if ((reinterpret_cast<uintptr_t>(start) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < kOwn; i += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(start + first + i);
+          s[i] = f.x, s[i + 1] = f.y, s[i + 2] = f.z, s[i + 3] = f.w;
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) s[i] = start[first + i];
@@ -668,6 +674,10 @@ __global__ void __launch_bounds__(Cfg<D, TOTAL>::kThreads, 1) tc_kernel(const __
       if (end && m.transposed) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) end[first + i * D] = s[i];
+      } else if (end && (reinterpret_cast<uintptr_t>(end) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < kOwn; i += 4)
+          *reinterpret_cast<float4 *>(end + first + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
       } else if (end) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) end[first + i] = s[i];

@@ -160,14 +160,15 @@ def attn(q, k, v, log_decay, cu_seqlens=None, scale=1.0, state_in=None, state_ou
     sequence's place in the states (without it, sequence i has place i); one
     that names no place, or another's, starts from zero and leaves no state.
     Rows outside every sequence are not written."""
-    shape, o, nbytes = _plan_attn(q, k, v, log_decay, cu_seqlens, state_in, state_out, slots, seqs, out)
     device = q.device
+    stream = _stream(device)
+    shape, o, nbytes = _plan_attn(q, k, v, log_decay, cu_seqlens, state_in, state_out, slots, seqs, out)
     if out is None:
         out = torch.empty(o, dtype=q.dtype, device=device)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     _call("slim_decay_fwd", q.dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(cu_seqlens),
           _ptr(state_in), _ptr(state_out), _ptr(slots), out.data_ptr(), ctypes.byref(shape), scale, ws.data_ptr(), nbytes,
-          _stream(device))
+          stream)
     return out
 
 
@@ -192,13 +193,14 @@ def attn_bwd(q, k, v, log_decay, do, cu_seqlens=None, scale=1.0, state_in=None, 
     """(dq, dk, dv) of :func:`attn`: do is the gradient of o, g_in (or None)
     that of the states behind the last rows; g_out (or None) receives that of
     state_in.  out: buffers for the three, whose rows may lie apart."""
-    shape, nbytes = _plan_bwd(q, k, v, log_decay, do, cu_seqlens, state_in, g_in, g_out, seqs, out)
     device = q.device
+    stream = _stream(device)
+    shape, nbytes = _plan_bwd(q, k, v, log_decay, do, cu_seqlens, state_in, g_in, g_out, seqs, out)
     dq, dk, dv = out if out is not None else (torch.empty(t.shape, dtype=q.dtype, device=device) for t in (q, k, v))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     _call("slim_decay_bwd", q.dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(cu_seqlens),
           do.data_ptr(), _ptr(state_in), _ptr(g_in), _ptr(g_out), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-          ctypes.byref(shape), scale, ws.data_ptr(), nbytes, _stream(device))
+          ctypes.byref(shape), scale, ws.data_ptr(), nbytes, stream)
     return dq, dk, dv
 
 
@@ -220,10 +222,11 @@ def step(q, k, v, log_decay, state, slots=None, scale=1.0, out=None):
     -> o [B, Hq, dv]; ``state`` is advanced in place.  slots: int32 [B], each
     row's place in it (without it, row i has place i); a row that names no
     place, or an earlier row's, gets zeros."""
-    shape, o = _plan_step(q, k, v, log_decay, state, slots, out)
     device = q.device
+    stream = _stream(device)
+    shape, o = _plan_step(q, k, v, log_decay, state, slots, out)
     if out is None:
         out = torch.empty(o, dtype=q.dtype, device=device)
     _call("slim_decay_step", q.dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
-          _ptr(slots), out.data_ptr(), ctypes.byref(shape), scale, _stream(device))
+          _ptr(slots), out.data_ptr(), ctypes.byref(shape), scale, stream)
     return out

@@ -136,6 +136,7 @@ CASES = {
     "long": ([2000], 2, 1, 64, 64, {}),
     "long_128": ([1500, 700], 1, 2, 128, 128, {}),
     "many_query_heads_64": ([140, 300, 20], 1, 9, 64, 64, {}),
+    "seven_query_heads_64": ([260, 129], 1, 7, 64, 64, {}),
     "many_query_heads_128": ([140, 300], 1, 5, 128, 128, {}),
     "group_of_four_128": ([290, 1, 128], 2, 4, 128, 128, dict(gap=(1, 2))),
     "group_of_four_64": ([290, 1, 128], 2, 4, 64, 64, dict(gap=(1, 2))),
