@@ -346,12 +346,15 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float *__restrict_
   }
 }
 
-// Blocks along the rows: at most as many as run at a time, four blocks of
-// eight warps an SM, and no more than the rows need.
-int row_blocks(int rows, int slabs) {
+// Blocks along the rows: at most as many as run at a time, `each` of eight
+// warps an SM, and no more than the rows need.  At 65536 x 1024 the forward
+// takes 67 us with four and 89 with two, the backward, whose registers leave
+// room for two, 131 with two and 136 with four.
+constexpr int kForwardBlocks = 4, kBackwardBlocks = 2;
+int row_blocks(int rows, int slabs, int each) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int most = (4 * sms + slabs - 1) / slabs, need = (rows + kWarps - 1) / kWarps;
+  const int most = (each * sms + slabs - 1) / slabs, need = (rows + kWarps - 1) / kWarps;
   return max(1, min(min(most, need), 65535));
 }
 
@@ -394,7 +397,7 @@ cudaError_t group_norm(const void *x, const float *gamma, const float *beta, con
   ProfScope ps("group_norm", st);
   const Shape s = shape_of(rows, cols, groups, eps, gate_row, 0);
   const Cut c = cut_for(cols, groups, gate_row % 8 == 0 && q8::vector_rows(cols, {x, gate, y}));
-  const dim3 grid(c.slabs(groups), row_blocks(rows, c.slabs(groups)));
+  const dim3 grid(c.slabs(groups), row_blocks(rows, c.slabs(groups), kForwardBlocks));
   const T *xp = static_cast<const T *>(x), *zp = static_cast<const T *>(gate);
   T *yp = static_cast<T *>(y);
   if (c.n == 0) {
@@ -414,7 +417,7 @@ cudaError_t group_norm(const void *x, const float *gamma, const float *beta, con
 // Blocks' column sums, for the cut with the most blocks along the rows.
 size_t group_norm_bwd_workspace(int rows, int cols, int groups) {
   int most = 1;
-  for (bool vec : {false, true}) most = max(most, row_blocks(rows, cut_for(cols, groups, vec).slabs(groups)));
+  for (bool vec : {false, true}) most = max(most, row_blocks(rows, cut_for(cols, groups, vec).slabs(groups), kBackwardBlocks));
   return sizeof(float) * 2 * (size_t)most * cols;
 }
 
@@ -426,7 +429,7 @@ cudaError_t group_norm_bwd(const void *dy, const void *x, const float *gamma, co
   const Shape s = shape_of(rows, cols, groups, eps, gate_row, dgate_row);
   const Cut c = cut_for(cols, groups,
                         gate_row % 8 == 0 && dgate_row % 8 == 0 && q8::vector_rows(cols, {dy, x, gate, dx, dgate}));
-  const dim3 grid(c.slabs(groups), row_blocks(rows, c.slabs(groups)));
+  const dim3 grid(c.slabs(groups), row_blocks(rows, c.slabs(groups), kBackwardBlocks));
   const T *dp = static_cast<const T *>(dy), *xp = static_cast<const T *>(x), *zp = static_cast<const T *>(gate);
   T *dxp = static_cast<T *>(dx), *dzp = static_cast<T *>(dgate);
   float *parts = dgamma || dbeta ? static_cast<float *>(workspace) : nullptr;
