@@ -10,8 +10,8 @@
 //   within   W = (S . decay) c    128 x D x 128   (the weighted scores as bf16, from tensor memory)
 //   update   U = b~^T c           D x D x 128     (b~: the rows with their weight to the tile's end)
 // and out = read factor * R + within factor * W, state = lambda^n state + U.
-// The weights lambda^(i-j) are formed as products of two powers of at most 1,
-// so that nothing overflows however strong the decay.
+// The weights lambda^(i-j) are products of two powers of at most 1, or come
+// from a table of powers, so that nothing overflows however strong the decay.
 //
 // Roundings: out is rounded once; weighted scores and X are bf16 operands,
 // each off by 2^-9 of a term in the mean square, like the result itself.  The
@@ -19,10 +19,14 @@
 // and remainder, 2^-17), because states are results in fp32 too.
 //
 // Roles: one warp loads tiles by TMA into a ring, two issue the MMAs, and
-// three warpgroups form the weighted scores; weigh b's rows and write the
-// results; and keep the state.  The bound is memory: 128 rows of four arrays take 2900 cycles of
-// this SM's share of HBM at D = 64 (5800 at 128), the products of a unit 1400
-// (2700).
+// warpgroups form the weighted scores; weigh b's rows; write the results (at
+// D = 64 in a warpgroup of its own); and keep the state.  The floor is memory:
+// 128 rows of four arrays take 2900 cycles of this SM's share of HBM at D = 64
+// (5800 at 128), the products of a unit 1700 (2700).  Measured over 2^20 rows
+// of 8 heads of 64: 2980 cycles a tile, 1600 for the totals, whose two arrays
+// take 1450.  At D = 128 a unit takes 7200: tensor memory has room for one
+// buffer of scores, and shared memory for five tiles, so that loads, scores,
+// weights and products of one unit follow one another.
 #pragma once
 
 #include "decay_common.cuh"
