@@ -568,6 +568,8 @@ size_t slim_group_norm_bwd_workspace_bytes(int rows, int cols, int groups);
  * For every element of every tensor that has a gradient, t = count[0] + 1:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
  *   p = (1 - lr wd) p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * m and v are formed in fp32, each product, sum and (with bits = 8) root
+ * rounded to nearest, 1 - beta from the double.
  * p is fp32, g bf16 (slim_adamw) or fp32 (slim_adamw_f32).  bits = 32: m and v
  * are fp32.  bits = 8: m, and in the place of v its root r = sqrt(v), are 8-bit
  * matrices of one row and n columns (see slim_q8_codes_bytes; zeros to begin
@@ -593,9 +595,9 @@ typedef struct {
 } slim_adamw_tensor;
 
 typedef struct {
-  float lr, beta1, beta2, eps, weight_decay;
+  float lr, eps, weight_decay;
   int bits;
-  double log_beta1, log_beta2;   /* natural logarithms (-inf for beta = 0) */
+  double beta1, beta2;
   unsigned long long seed;
   const float *lr_device;        /* NULL, or where the kernel reads lr when it runs */
 } slim_adamw_options;

@@ -93,7 +93,7 @@ slim_status run_norm_bwd(const void *dy, const void *x, const float *gamma, cons
                 st);
 }
 
-bool fraction(float b) { return b >= 0.f && b < 1.f; }
+bool fraction(double b) { return b >= 0.0 && b < 1.0; }
 
 slim_status run_adamw(const slim_adamw_tensor *tensors, int n, const slim_adamw_options *options, int *count,
                       bool g_f32, cudaStream_t st) {

@@ -8,7 +8,6 @@ Marshalling for ``slim_adamw``; the step runs in the library's CUDA kernel.
     layer.load(wqkv=weights[0], ...)      # and are packed again
 """
 import ctypes
-import math
 
 import torch
 
@@ -25,8 +24,8 @@ class _Tensor(ctypes.Structure):
 
 class _Options(ctypes.Structure):
     """slim_adamw_options."""
-    _fields_ = [(n, _f) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [("bits", _i)] \
-        + [("log_beta1", ctypes.c_double), ("log_beta2", ctypes.c_double), ("seed", ctypes.c_ulonglong), ("lr_device", _vp)]
+    _fields_ = [(n, _f) for n in ("lr", "eps", "weight_decay")] + [("bits", _i)] \
+        + [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("seed", ctypes.c_ulonglong), ("lr_device", _vp)]
 
 
 for _fn in (_lib.slim_adamw, _lib.slim_adamw_f32):
@@ -82,10 +81,7 @@ class AdamW:
             self._check_state(b, p)
         self._refuse_overlaps()
         self.count = torch.tensor([count, 0], dtype=torch.int32, device=device)
-        log = lambda b: math.log(b) if b > 0 else -math.inf
-        # the logarithms of the fp32 numbers that the kernel multiplies with
-        rounded = [ctypes.c_float(b).value for b in betas]
-        self._options = _Options(0.0, rounded[0], rounded[1], eps, weight_decay, bits, log(rounded[0]), log(rounded[1]), seed, None)
+        self._options = _Options(0.0, eps, weight_decay, bits, betas[0], betas[1], seed, None)
         self._tensors = (_Tensor * len(self.params))()
         for t, p, a, b in zip(self._tensors, self.params, self.m, self.v):
             t.param, t.n = p.data_ptr(), p.numel()
